@@ -63,6 +63,7 @@ typedef enum {
 } ubw_status;
 
 enum { UBW_F32 = 0, UBW_F16 = 1 };                       /* activation dtypes */
+enum { UBW_BF16 = 2, UBW_E4M3 = 3 };                     /* more types of the key/value cache calls */
 enum { UBW_SRC_CANON_BITS = 0, UBW_SRC_INT8_SIGNS = 1 };  /* ubw_pack_bases sources */
 
 /* Largest batch one GEMV call accepts. At group width 8 a batch runs in one launch on the
@@ -420,6 +421,190 @@ int ubw_lut_gemv_geometry(const uint32_t* packed, const void* alpha_r, const flo
  * Errors: UBW_EINVAL (null, bytes < 16 or not a multiple of 16), UBW_EALIGN, UBW_EHIP.
  */
 int ubw_bench_stream_read(const void* buf, int64_t bytes, uint32_t* out, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Between the q, k, v products and the o product of a decoder layer: keys and values in a paged
+ * cache, attention over it, and the cache's pages. The products take up to UBW_MAX_BATCH rows, so a
+ * decoding step of a sequence is one token or a tree of drafted tokens; these calls take trees of
+ * up to UBW_MAX_TREE tokens for each sequence of a batch.
+ *
+ * The cache: pages of page_size tokens each. Token slot t lies in page t / page_size at row
+ * t % page_size; a sequence's tokens are at the pages of its table row: position p of sequence b is
+ * row p % page_size of page table[b][p / page_size].
+ * Values are fp16, bf16, or OCP e4m3 (1-4-3, largest 448, no infinities): an e4m3 element x of head
+ * h stands for x * scale[h].
+ */
+#define UBW_MAX_TREE 64   /* most tokens of one sequence in an attention call */
+#define UBW_MAX_SEQS 4096 /* most sequences of one attention call or page pool */
+
+/* Host struct; the pointers in it are device pointers. Element (layer l, page p, head h, row r,
+ * dim d) of k is at k + l k_stride[0] + p k_stride[1] + h k_stride[2] + r k_stride[3] + d, in
+ * elements (v the same with v_stride). Pages and rows of one cache do not overlap. */
+typedef struct ubw_kv_cache {
+    void* k;
+    void* v;
+    int dtype;               /* UBW_F16, UBW_BF16 or UBW_E4M3 */
+    int layers;              /* layers of the copying calls; the others take the first one */
+    int pages;
+    int page_size;           /* a power of two, 16 to 1024 */
+    int kv_heads;
+    int head_dim;            /* 64, 128 or 256 */
+    int64_t k_stride[4];     /* layer, page, head, row; multiples of 16 bytes */
+    int64_t v_stride[4];
+    const float* k_scale;    /* [kv_heads], positive, e4m3 only; NULL: 1 */
+    const float* v_scale;
+} ubw_kv_cache;
+
+/*
+ * Norms of queries and keys for each head, their position rotation, and the store of keys and
+ * values into the cache, in one pass over the projections' outputs.
+ *   for each token t and head: y = x * (mean(x^2) + eps)^(-1/2) * w   (w NULL: y = x)
+ *   z: for i < rot / 2 the pair (a, b) at angle positions[t] * inv_freq[i] becomes
+ *      (a cos - b sin, b cos + a sin); dims from rot on stay y. Pairs are (i, i + rot / 2), or with
+ *      interleaved != 0 (2 i, 2 i + 1). Angles are taken in 64 bits, so far positions stay exact.
+ *   q_out[t][h] = z of q;  cache.k at slot slots[t] = z of k;  cache.v there = v.
+ * Norm and rotation are computed in fp32 and rounded once, to nearest even; e4m3 elements are
+ * value / scale[h], values beyond 448 become 448 of their sign, a NaN stays a NaN.
+ *   q, k, v    in_dtype (UBW_F32, UBW_F16, UBW_BF16), token t's heads x head_dim values at
+ *              q + t * ldq (ldk, ldv), contiguous; rows 16-byte aligned (rows of a fused buffer do)
+ *   q_weight, k_weight  fp32 [head_dim] or NULL (no norm)
+ *   positions  int32 [tokens]; slots int32 [tokens]: a token whose slot is outside
+ *              [0, pages * page_size) has its keys and values not stored (its q_out is written).
+ *              Slots that are stored must differ from one another.
+ *   inv_freq   fp32 [rot / 2]; rot is even, 0 (no rotation) to head_dim; pairs (i, i + rot / 2)
+ *              need rot a multiple of head_dim / 8
+ *   q_out      out_dtype (UBW_F16, UBW_BF16), token t at q_out + t * ldo, 16-byte aligned rows
+ * tokens = 0 is allowed and enqueues nothing.
+ * Errors: UBW_EINVAL (null, sizes, eps negative or not finite, a row stride below its row),
+ *         UBW_EUNSUPPORTED (types, head_dim, page_size, rot), UBW_EALIGN, UBW_ERANGE (strides that
+ *         pass 2 GiB within 16 rows of a page, 2^24 tokens or more), UBW_EHIP.
+ */
+int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                     const void* v, int64_t ldv, int in_dtype, int64_t tokens, int heads, const float* q_weight,
+                     const float* k_weight, float eps, const float* inv_freq, int rot, int interleaved,
+                     const int32_t* positions, const int32_t* slots, void* q_out, int out_dtype, int64_t ldo,
+                     void* stream);
+
+/*
+ * Attention of each sequence's newest tokens over its cached context and over one another, by a
+ * mask of their tree. Sequence b has the tokens (rows of q) q_start[b] .. q_start[b + 1] - 1, n of
+ * them, and ctx_len[b] = L positions of context; its token i has its key and value at position
+ * L + i (stored by ubw_qk_norm_rope before). Token i sees every position below L, and position
+ * L + j (j < n) where bit j of masks[q_start[b] + i] is set (masks NULL: where j <= i).
+ *   s_j = scale * q . k_j over the positions seen;  out = sum softmax(s)_j v_j;  lse = log sum exp s
+ * A token that sees nothing gets out = 0 and lse = -infinity. Positions not seen contribute
+ * nothing, whatever their values (NaN and infinities included). Query head h reads key/value head
+ * h / (heads / kv_heads). Scores, softmax and sums are fp32; the weights are rounded to q's type for
+ * the product with v.
+ *   q, out     q_dtype (UBW_F16 or UBW_BF16; the cache's type unless that is UBW_E4M3), token t's
+ *              heads x head_dim at q + t * ldq (out + t * ldo), 16-byte aligned rows
+ *   q_start    int32 [batch + 1] ascending, q_start[batch] <= tokens; rows of out and lse that
+ *              belong to no sequence are left as they were
+ *   ctx_len    int32 [batch] (below 0 counts as 0)
+ *   table      int32 [batch][ld_table], table_cols columns used. Positions beyond
+ *              table_cols * page_size, or on a page outside [0, pages), are not seen.
+ *   max_tree   the largest n, at most UBW_MAX_TREE (a sequence's tokens beyond it are not written)
+ *   max_len    the largest L + n (it only steers the split over workgroups); 0: unknown
+ *   masks      uint64 [tokens] or NULL;  lse fp32 [tokens][heads] or NULL
+ *   workspace  ubw_tree_attn_workspace_bytes() bytes of scratch, or NULL with 0 bytes. With it long
+ *              contexts are split over workgroups and joined by a second launch (in a fixed order:
+ *              results do not vary from run to run). It needs no initialization and keeps nothing
+ *              between calls; calls that may run at the same time need their own.
+ * Nothing in device memory is trusted for addresses: lengths, starts and table entries out of range
+ * are cut as above. tokens = 0 or batch = 0 enqueues nothing.
+ * Errors: UBW_EINVAL (null, sizes, heads no multiple of kv_heads, scale not positive and finite),
+ *         UBW_EUNSUPPORTED (types, head_dim, page_size), UBW_ERANGE (batch above UBW_MAX_SEQS,
+ *         max_tree, strides, 2^24 pieces of work or more), UBW_EALIGN, UBW_ESIZE (workspace), UBW_EHIP.
+ */
+int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_heads, int head_dim, size_t* out);
+int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+                  const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table,
+                  int64_t ld_table, int table_cols, int max_tree, int64_t max_len, const uint64_t* masks,
+                  float scale, void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Copies whole pages, keys and values of every layer: page pairs[i][0] to page pairs[i][1]. A pair
+ * with an entry outside [0, pages) is skipped. No page may be the target of two pairs, or the
+ * target of one and the source of another (its contents are then unspecified; nothing else is).
+ *   pairs  int32 [count][2], e.g. as ubw_pages_reserve leaves them
+ * count = 0 enqueues nothing.
+ * Errors: as ubw_qk_norm_rope for the cache; UBW_ERANGE (count above 2^20, 2^24 or more pieces of
+ *         16 KiB in one page of all layers).
+ */
+int ubw_cache_copy_pages(const ubw_kv_cache* cache, const int32_t* pairs, int64_t count, void* stream);
+
+/*
+ * Draws kept tokens together behind a context, in every layer: for each sequence b, the key and
+ * value at position ctx_len[b] + keep[b][i] move to position ctx_len[b] + i, for i = 0, 1, ... in
+ * order. A list ends at its first entry that is negative or not above the entry before it (so
+ * keep[b][i] >= i and nothing is overwritten before it is read). Positions beyond the table or on a
+ * page outside [0, pages) are not moved. Positions behind the kept ones keep what they hold.
+ *   table  int32 [batch][ld_table]; sequences whose written pages are shared are the caller's
+ *          business (ubw_pages_reserve gives a sequence its own copy before it writes)
+ *   keep   int32 [batch][width]
+ * batch = 0 or width = 0 enqueues nothing.
+ * Errors: as ubw_cache_copy_pages; UBW_ERANGE (batch above UBW_MAX_SEQS, width above 1024).
+ */
+int ubw_cache_compact(const ubw_kv_cache* cache, const int32_t* table, int64_t ld_table, int table_cols,
+                      const int32_t* ctx_len, const int32_t* keep, int width, int batch, void* stream);
+
+/*
+ * The pages of a cache shared out over sequences, in device memory (host struct of device
+ * pointers): who holds which page, with counts, so that sequences can share pages. The calls below
+ * keep: ref[p] = number of table entries that hold page p; bit p % 32 of free_bits[p / 32] set
+ * where ref[p] == 0 (bits past the last page 0); row s of table has held[s] pages, then -1;
+ * len[s] <= held[s] * page_size tokens. All results are whole numbers that do not depend on timing.
+ * One pool serves one stream at a time.
+ * status collects faults (bits stay until the caller clears the word):
+ *   bit 0: not enough free pages (that ubw_pages_reserve call reserved nothing)
+ *   bit 1: an entry that cannot be served (see the calls; that sequence is left as it was)
+ */
+typedef struct ubw_page_pool {
+    int32_t* ref;         /* [pages] */
+    uint32_t* free_bits;  /* [ceil(pages / 32)] */
+    int32_t* table;       /* [seqs][max_pages], contiguous */
+    int32_t* held;        /* [seqs] */
+    int32_t* len;         /* [seqs] */
+    uint32_t* status;     /* [1] */
+    int pages;            /* 1 to 2^24 */
+    int page_size;        /* a power of two, 16 to 1024 */
+    int seqs;             /* 1 to UBW_MAX_SEQS */
+    int max_pages;        /* table columns */
+} ubw_page_pool;
+
+/* An empty pool: every page free, every sequence without pages, status 0.
+ * Errors: UBW_EINVAL (null, sizes), UBW_EUNSUPPORTED (page_size), UBW_ERANGE, UBW_EHIP. */
+int ubw_pages_init(const ubw_page_pool* pool, void* stream);
+
+/*
+ * Sets sequence s to new_len[s] tokens where that is not negative, and gives back the pages behind
+ * them (0: the sequence is freed; a page is free when its last holder gives it back). It may also
+ * raise len, within the pages held (after tokens were stored in reserved room). More than
+ * held[s] * page_size is an entry that cannot be served.
+ *   new_len  int32 [seqs]
+ */
+int ubw_pages_trim(const ubw_page_pool* pool, const int32_t* new_len, void* stream);
+
+/*
+ * Forks: sequence s becomes a copy of sequence parents[s] where that is not negative, by sharing
+ * the pages that hold the parent's len tokens (nothing is copied). Entries that cannot be served: a
+ * parent outside [0, seqs), s itself or itself a fork of this call; an s that holds pages.
+ *   parents  int32 [seqs]
+ */
+int ubw_pages_fork(const ubw_page_pool* pool, const int32_t* parents, void* stream);
+
+/*
+ * Room for room[s] more tokens behind len[s] of each sequence where that is positive: pages are
+ * taken from the free ones, the lowest first, sequence by sequence. Where the first of the new
+ * tokens falls on a page that others hold too, the sequence gets a page of its own for it (taken
+ * before its other pages) and pairs[s] = (old page, new page); pairs[s] = (-1, -1) elsewhere. Pass
+ * pairs to ubw_cache_copy_pages, with the cache, before the next call on the pool. (Where all
+ * holders of such a page ask at once, each gets a copy and the page is given back.) len stays;
+ * ubw_pages_trim sets it once tokens are stored. An entry that needs more than max_pages pages
+ * cannot be served.
+ *   room   int32 [seqs];  pairs  int32 [seqs][2], fully written
+ */
+int ubw_pages_reserve(const ubw_page_pool* pool, const int32_t* room, int32_t* pairs, void* stream);
 
 #ifdef __cplusplus
 }

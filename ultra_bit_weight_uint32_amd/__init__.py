@@ -21,10 +21,11 @@ UBW_OK = 0
 UBW_EINVAL, UBW_EUNSUPPORTED, UBW_EALIGN = -1, -2, -3
 UBW_ERANGE = -4
 UBW_EHIP, UBW_ESIZE, UBW_EWAIT = -5, -6, -7
-UBW_F32, UBW_F16 = 0, 1
+UBW_F32, UBW_F16, UBW_BF16, UBW_E4M3 = 0, 1, 2, 3
 UBW_SRC_CANON_BITS, UBW_SRC_INT8_SIGNS = 0, 1
 MAX_BATCH = 16
 MAX_GROUP = 8
+MAX_TREE, MAX_SEQS = 64, 4096
 
 # every symbol include/ubw.h declares
 EXPORTS = (
@@ -34,6 +35,8 @@ EXPORTS = (
     "ubw_check_indices", "ubw_extract_patterns", "ubw_lut_gemv_geometry", "ubw_bench_stream_read",
     "ubw_lut_gemv_multi", "ubw_lut_gemv_gs", "ubw_fit_workspace_bytes", "ubw_fit_bases",
     "ubw_gram", "ubw_saliency_workspace_bytes", "ubw_hessian_saliency",
+    "ubw_qk_norm_rope", "ubw_tree_attn_workspace_bytes", "ubw_tree_attn", "ubw_cache_copy_pages",
+    "ubw_cache_compact", "ubw_pages_init", "ubw_pages_trim", "ubw_pages_fork", "ubw_pages_reserve",
 )
 
 
@@ -44,6 +47,25 @@ class GemvDesc(ctypes.Structure):
         ("idx", ctypes.c_void_p), ("s", ctypes.c_int64), ("packed_s", ctypes.c_void_p),
         ("alpha_r_s", ctypes.c_void_p), ("alpha_c_s", ctypes.c_void_p), ("ns", ctypes.c_int), ("N", ctypes.c_int64),
         ("y", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """Mirror of ubw_kv_cache (include/ubw.h)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("layers", ctypes.c_int),
+        ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 4), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class PagePoolDesc(ctypes.Structure):
+    """Mirror of ubw_page_pool (include/ubw.h)."""
+    _fields_ = [
+        ("ref", ctypes.c_void_p), ("free_bits", ctypes.c_void_p), ("table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+        ("len", ctypes.c_void_p), ("status", ctypes.c_void_p), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("seqs", ctypes.c_int), ("max_pages", ctypes.c_int),
     ]
 
 
@@ -91,6 +113,18 @@ def lib():
         "ubw_saliency_workspace_bytes": ([I64, I64, ctypes.POINTER(SZ)], I),
         "ubw_hessian_saliency": ([P, I64, ctypes.c_float, P, I64, I64, P, P, P, P, SZ, P], I),
     }
+    C, PP, F = ctypes.POINTER(KVCacheDesc), ctypes.POINTER(PagePoolDesc), ctypes.c_float
+    sig.update({
+        "ubw_qk_norm_rope": ([C, P, I64, P, I64, P, I64, I, I64, I, P, P, F, P, I, I, P, P, P, I, I64, P], I),
+        "ubw_tree_attn_workspace_bytes": ([I, I, I, I, I, ctypes.POINTER(SZ)], I),
+        "ubw_tree_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, I, I64, P, F, P, I64, P, P, SZ, P], I),
+        "ubw_cache_copy_pages": ([C, P, I64, P], I),
+        "ubw_cache_compact": ([C, P, I64, I, P, P, I, I, P], I),
+        "ubw_pages_init": ([PP, P], I),
+        "ubw_pages_trim": ([PP, P, P], I),
+        "ubw_pages_fork": ([PP, P, P], I),
+        "ubw_pages_reserve": ([PP, P, P, P], I),
+    })
     for name, (args, res) in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -596,3 +630,19 @@ def bench_stream_read(buf, nbytes: int, out):
     """Measurement helper: one streaming read of nbytes of buf (see include/ubw.h)."""
     _check("ubw_bench_stream_read", lib().ubw_bench_stream_read(_dev(buf, "buf", None), int(nbytes),
                                                                 _dev(out, "out", None), _stream()))
+
+
+
+# ---------------------------------------------------------------------------------------------
+# keys and values in a paged cache (cache.py, loaded with torch on first use)
+
+_CACHE_CALLS = ("KVCache", "PagePool", "cache_compact", "cache_copy_pages", "page_pool", "pages_fork", "pages_reserve",
+                "pages_trim", "qk_norm_rope", "tree_attn", "tree_attn_workspace")
+
+
+def __getattr__(name):
+    if name in _CACHE_CALLS:
+        from . import cache
+        globals().update({n: getattr(cache, n) for n in _CACHE_CALLS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,286 @@
+"""Keys and values in a paged cache: the store with norm and rotation, attention over the cache, and
+its pages. Thin marshalling over the calls of include/ubw.h, like the rest of the package.
+
+A decoding step of a batch, for one layer:
+
+    q, k, v = the products (lut_gemv_multi)                      [tokens, heads, head_dim]
+    qk_norm_rope(q, k, v, cache, positions, slots, inv_freq)     keys and values into the cache
+    tree_attn(q, cache, pool.table, q_start, pool.len, masks)    the input of the o product
+
+and once per step, for all layers: pages_reserve before it, cache_compact (of the drafted tokens that
+were accepted) and pages_trim behind it.
+
+KVCache and PagePool hold the tensors and their descriptors, checked once; the calls check what
+changes from call to call. Every call runs on its tensors' device, on that device's current stream.
+"""
+import ctypes
+import math
+
+import torch
+
+from . import (UBW_BF16, UBW_E4M3, UBW_F16, UBW_F32, KVCacheDesc, PagePoolDesc, _check, lib)
+
+_TYPES = {torch.float32: UBW_F32, torch.float16: UBW_F16, torch.bfloat16: UBW_BF16, torch.float8_e4m3fn: UBW_E4M3}
+
+
+class _On:
+    """The device of a call: its stream, made current for the launch where it is not."""
+    __slots__ = ("device", "before")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _flat(t, name, dtype, device, numel=None, shape=None, at_least=False):
+    """Pointer of a contiguous tensor of a dtype on the call's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if numel is not None and (t.numel() < numel if at_least else t.numel() != numel):
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows(t, name, device, dim, heads=None, tokens=None, dtype=None):
+    """(pointer, row stride) of [tokens, heads, dim] whose heads are contiguous; rows may be apart (a
+    part of a fused buffer)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or \
+            (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name} must be [{tokens if tokens is not None else 'tokens'}, "
+                         f"{heads if heads is not None else 'heads'}, {dim}], got {list(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    st = t.stride()
+    if st[2] != 1 or (t.shape[1] > 1 and st[1] != dim):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else t.shape[1] * dim
+
+
+class KVCache:
+    """A paged cache: k and v [layers, pages, kv_heads, page_size, head_dim] (or without layers), fp16,
+    bf16 or float8_e4m3fn, any strides with contiguous head_dim (token-major caches as views).
+    k_scale, v_scale: fp32 [kv_heads], what 8-bit elements are multiplied by (default 1)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not k.is_cuda:
+            raise ValueError("k must be on a GPU (no CPU path exists)")
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must have the same shape, dtype and device")
+        if k.dim() not in (4, 5):
+            raise ValueError("k must be [layers, pages, kv_heads, page_size, head_dim] or without layers")
+        if k.dtype not in (torch.float16, torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"k has dtype {k.dtype}, expected float16, bfloat16 or float8_e4m3fn")
+        if k.stride(-1) != 1 or v.stride(-1) != 1:
+            raise ValueError("head_dim must be contiguous")
+        if k.dtype is not torch.float8_e4m3fn and (k_scale is not None or v_scale is not None):
+            raise ValueError("scales belong to 8-bit caches")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.dtype = k.device, k.dtype
+        k5, v5 = (x if x.dim() == 5 else x[None] for x in (k, v))
+        self.layers, self.pages, self.kv_heads, self.page_size, self.head_dim = k5.shape
+        d = KVCacheDesc()
+        d.k, d.v, d.dtype = k.data_ptr(), v.data_ptr(), _TYPES[k.dtype]
+        d.layers, d.pages, d.page_size, d.kv_heads, d.head_dim = (self.layers, self.pages, self.page_size,
+                                                                  self.kv_heads, self.head_dim)
+        d.k_stride[:], d.v_stride[:] = k5.stride()[:4], v5.stride()[:4]
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is not None:
+                setattr(d, name, _flat(s, name, torch.float32, self.device, numel=self.kv_heads))
+        self.desc, self.ref = d, ctypes.byref(d)
+
+    def layer(self, i):
+        """The cache of one layer, as the calls of that layer take it."""
+        if self.k.dim() != 5:
+            raise ValueError("this cache has one layer")
+        return KVCache(self.k[i], self.v[i], self.k_scale, self.v_scale)
+
+
+def qk_norm_rope(q, k, v, cache, positions, slots, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, out=None, out_dtype=None):
+    """Norms of queries and keys for each head (weights fp32 [head_dim], None: no norm), rotation at
+    positions (int32 [tokens]) by inv_freq (fp32 [rot / 2], None: no rotation), keys and values stored
+    at slots (int32 [tokens]; outside the cache: not stored) of the cache. q [tokens, heads, head_dim],
+    k, v [tokens, kv_heads, head_dim] in fp32, fp16 or bf16. Returns the queries [tokens, heads,
+    head_dim] in out (or a new tensor of out_dtype; default the cache's type, fp16 for 8 bits)."""
+    dev, dim, kvh = cache.device, cache.head_dim, cache.kv_heads
+    qp, ldq = _rows(q, "q", dev, dim)
+    t, heads = q.shape[0], q.shape[1]
+    kp, ldk = _rows(k, "k", dev, dim, kvh, t, q.dtype)
+    vp, ldv = _rows(v, "v", dev, dim, kvh, t, q.dtype)
+    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError(f"q has dtype {q.dtype}, expected float32, float16 or bfloat16")
+    if out is None:
+        if out_dtype is None:
+            out_dtype = torch.float16 if cache.dtype is torch.float8_e4m3fn else cache.dtype
+        out = torch.empty((t, heads, dim), dtype=out_dtype, device=dev)
+    if out.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"out has dtype {out.dtype}, expected float16 or bfloat16")
+    op, ldo = _rows(out, "out", dev, dim, heads, t)
+    f32, i32 = torch.float32, torch.int32
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    with _On(dev) as stream:
+        _check("ubw_qk_norm_rope", lib().ubw_qk_norm_rope(
+            cache.ref, qp, ldq, kp, ldk, vp, ldv, _TYPES[q.dtype], t, heads,
+            None if q_weight is None else _flat(q_weight, "q_weight", f32, dev, dim),
+            None if k_weight is None else _flat(k_weight, "k_weight", f32, dev, dim), eps,
+            None if rot == 0 else _flat(inv_freq, "inv_freq", f32, dev), rot, 1 if interleaved else 0,
+            _flat(positions, "positions", i32, dev, t), _flat(slots, "slots", i32, dev, t), op, _TYPES[out.dtype], ldo,
+            stream))
+    return out
+
+
+def tree_attn_workspace(batch, max_tree, heads, kv_heads, head_dim, device="cuda"):
+    """Scratch for tree_attn calls of up to these sizes (reusable on one stream)."""
+    n = ctypes.c_size_t()
+    _check("ubw_tree_attn_workspace_bytes",
+           lib().ubw_tree_attn_workspace_bytes(batch, max_tree, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return torch.empty(-(-n.value // 4), dtype=torch.float32, device=device)
+
+
+def tree_attn(q, cache, table, q_start, ctx_len, masks=None, *, max_tree, max_len=0, scale=None, out=None, lse=None,
+              workspace=None):
+    """Attention of each sequence's new tokens (one, or a tree of up to 64 drafted ones) over its context
+    in the cache and over one another. q [tokens, heads, head_dim]; table int32 [batch, columns] (rows
+    may be apart); q_start int32 [batch + 1]; ctx_len int32 [batch]; masks int64 or uint64 [tokens], bit
+    j of a token's: it sees token j of its tree (None: those up to itself). max_tree: the most tokens a
+    sequence has; max_len: the longest context plus tokens (0: unknown). lse: None or fp32 [tokens,
+    heads] to be written. workspace: tree_attn_workspace() (None: long contexts are not split over
+    workgroups). Returns out [tokens, heads, head_dim] in q's type."""
+    dev, dim = cache.device, cache.head_dim
+    qp, ldq = _rows(q, "q", dev, dim)
+    t, heads = q.shape[0], q.shape[1]
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q has dtype {q.dtype}, expected float16 or bfloat16")
+    if out is None:
+        out = torch.empty((t, heads, dim), dtype=q.dtype, device=dev)
+    op, ldo = _rows(out, "out", dev, dim, heads, t, q.dtype)
+    i32 = torch.int32
+    batch = ctx_len.numel()
+    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not i32 or table.device != dev or \
+            table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be int32 [{batch}, columns] with contiguous columns on {dev}")
+    if masks is not None and masks.dtype not in (torch.int64, torch.uint64):
+        raise TypeError(f"masks has dtype {masks.dtype}, expected int64 or uint64")
+    ws, wsb = None, 0
+    if workspace is not None:
+        ws, wsb = _flat(workspace, "workspace", workspace.dtype, dev), workspace.numel() * workspace.element_size()
+    with _On(dev) as stream:
+        _check("ubw_tree_attn", lib().ubw_tree_attn(
+            cache.ref, qp, _TYPES[q.dtype], ldq, t, heads, _flat(q_start, "q_start", i32, dev, batch + 1),
+            _flat(ctx_len, "ctx_len", i32, dev), batch, table.data_ptr(),
+            table.stride(0) if batch > 1 else table.shape[1], table.shape[1], max_tree, max_len,
+            None if masks is None else _flat(masks, "masks", masks.dtype, dev, t),
+            1 / math.sqrt(dim) if scale is None else scale, op, ldo,
+            None if lse is None else _flat(lse, "lse", torch.float32, dev, shape=(t, heads)), ws, wsb, stream))
+    return out
+
+
+def cache_copy_pages(cache, pairs):
+    """Page pairs[i, 0] copied to page pairs[i, 1] (int32 [count, 2]), keys and values of every layer.
+    Pairs with an entry outside the cache's pages, as (-1, -1), are skipped."""
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError(f"pairs must be [count, 2], got {list(pairs.shape)}")
+    with _On(cache.device) as stream:
+        _check("ubw_cache_copy_pages", lib().ubw_cache_copy_pages(
+            cache.ref, _flat(pairs, "pairs", torch.int32, cache.device), pairs.shape[0], stream))
+
+
+def cache_compact(cache, table, ctx_len, keep):
+    """Keys and values at position ctx_len[b] + keep[b, i] moved to ctx_len[b] + i in every layer, for
+    i = 0, 1, ... up to the first entry of keep (int32 [batch, width]) that does not ascend from 0."""
+    dev, i32 = cache.device, torch.int32
+    if keep.dim() != 2:
+        raise ValueError(f"keep must be [batch, width], got {list(keep.shape)}")
+    batch, width = keep.shape
+    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not i32 or table.device != dev or \
+            table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be int32 [{batch}, columns] with contiguous columns on {dev}")
+    with _On(dev) as stream:
+        _check("ubw_cache_compact", lib().ubw_cache_compact(
+            cache.ref, table.data_ptr(), table.stride(0) if batch > 1 else table.shape[1], table.shape[1],
+            _flat(ctx_len, "ctx_len", i32, dev, batch), _flat(keep, "keep", i32, dev), width, batch, stream))
+
+
+class PagePool:
+    """Pages shared out over sequences, in device memory (ubw_page_pool of include/ubw.h): ref int32
+    [pages], free int32 [ceil(pages / 32)] (a bit set), table int32 [seqs, max_pages], held and len
+    int32 [seqs], status int32 [1]. page_pool() makes an empty one."""
+
+    NO_PAGES, NOT_SERVED = 1, 2   # bits of status
+
+    def __init__(self, ref, free, table, held, len, status, page_size):
+        if not ref.is_cuda:
+            raise ValueError("ref must be on a GPU (no CPU path exists)")
+        self.ref, self.free, self.table, self.held, self.len, self.status = ref, free, table, held, len, status
+        self.device, self.page_size = ref.device, page_size
+        self.pages, (self.seqs, self.max_pages) = ref.numel(), table.shape
+        i32, dev = torch.int32, self.device
+        d = PagePoolDesc()
+        d.ref = _flat(ref, "ref", i32, dev)
+        d.free_bits = _flat(free, "free", i32, dev, numel=-(-self.pages // 32))
+        d.table = _flat(table, "table", i32, dev)
+        d.held = _flat(held, "held", i32, dev, numel=self.seqs)
+        d.len = _flat(len, "len", i32, dev, numel=self.seqs)
+        d.status = _flat(status, "status", i32, dev, numel=1)
+        d.pages, d.page_size, d.seqs, d.max_pages = self.pages, page_size, self.seqs, self.max_pages
+        self.desc, self.byref = d, ctypes.byref(d)
+
+
+def page_pool(pages, page_size, seqs, max_pages, device="cuda"):
+    """An empty pool: every page free, no sequence holding any."""
+    if pages < 1 or seqs < 1 or max_pages < 1:
+        raise ValueError("pages, seqs and max_pages must be positive")
+    new = [torch.empty(n, dtype=torch.int32, device=device)
+           for n in (pages, -(-pages // 32), (seqs, max_pages), seqs, seqs, 1)]
+    pool = PagePool(*new, page_size)
+    with _On(pool.device) as stream:
+        _check("ubw_pages_init", lib().ubw_pages_init(pool.byref, stream))
+    return pool
+
+
+def pages_trim(pool, new_len):
+    """len[s] = new_len[s] where that is not negative (int32 [seqs]), the pages behind it given back."""
+    p = _flat(new_len, "new_len", torch.int32, pool.device, pool.seqs)
+    with _On(pool.device) as stream:
+        _check("ubw_pages_trim", lib().ubw_pages_trim(pool.byref, p, stream))
+
+
+def pages_fork(pool, parents):
+    """Sequence s becomes a copy of parents[s] where that is not negative (int32 [seqs]), by sharing."""
+    p = _flat(parents, "parents", torch.int32, pool.device, pool.seqs)
+    with _On(pool.device) as stream:
+        _check("ubw_pages_fork", lib().ubw_pages_fork(pool.byref, p, stream))
+
+
+def pages_reserve(pool, room, pairs=None):
+    """Pages for room[s] more tokens of each sequence (int32 [seqs]). Returns pairs, int32 [seqs, 2]:
+    (old, new) where a sequence got its own copy of a shared page, to be passed to cache_copy_pages
+    before the pool's next call; (-1, -1) elsewhere."""
+    p = _flat(room, "room", torch.int32, pool.device, pool.seqs)
+    if pairs is None:
+        pairs = torch.empty((pool.seqs, 2), dtype=torch.int32, device=pool.device)
+    with _On(pool.device) as stream:
+        _check("ubw_pages_reserve", lib().ubw_pages_reserve(
+            pool.byref, p, _flat(pairs, "pairs", torch.int32, pool.device, shape=(pool.seqs, 2)), stream))
+    return pairs

@@ -1,0 +1,130 @@
+// Argument checks and launch planning of the key/value cache calls: plain integer arithmetic with
+// no HIP dependency, shared by the host code, the kernels (functions marked UBW_HD) and a host test
+// program built with address and undefined-behaviour sanitizers.
+#pragma once
+#include <stdint.h>
+
+#include "plan.h"
+
+namespace ubw {
+namespace cache {
+
+using plan::aligned16;
+using plan::cdiv;
+
+inline int type_size(int dtype) {
+    return dtype == UBW_F32 ? 4 : dtype == UBW_F16 || dtype == UBW_BF16 ? 2 : dtype == UBW_E4M3 ? 1 : 0;
+}
+// Workgroups of 256 threads in one grid dimension: work-items there are counted in 32 bits.
+constexpr int64_t kMaxGrid = (1 << 24) - 1;
+constexpr int kCopyVecs = 4;  // 16-byte vectors a copying thread has in flight
+
+inline bool page_size_ok(int ps) { return ps >= 16 && ps <= 1024 && (ps & (ps - 1)) == 0; }
+inline int log2_of(int pow2) {
+    int l = 0;
+    while ((1 << l) < pow2) ++l;
+    return l;
+}
+
+// Strides of k or v: multiples of 16 bytes, rows of a page reached from the page's first element
+// with 32-bit byte offsets over 16 rows, and offsets of the whole cache within 63 bits.
+inline int check_strides(const int64_t* st, const ubw_kv_cache& c, int size) {
+    const int64_t most = (int64_t)1 << 40;
+    const int64_t n[4] = {c.layers, c.pages, c.kv_heads, c.page_size};
+    for (int i = 0; i < 4; ++i) {
+        if (st[i] < 0 || st[i] > most) return UBW_ERANGE;
+        if ((st[i] * size) & 15) return UBW_EALIGN;
+        if (n[i] > 1 && st[i] < c.head_dim) return UBW_EINVAL;
+        if (st[i] > 0 && n[i] > ((int64_t)1 << 60) / st[i]) return UBW_ERANGE;
+    }
+    if (st[3] * size * 16 >= ((int64_t)1 << 31)) return UBW_ERANGE;
+    return UBW_OK;
+}
+
+inline int check_cache(const ubw_kv_cache* c) {
+    if (!c || !c->k || !c->v || c->layers < 1 || c->pages < 1 || c->kv_heads < 1) return UBW_EINVAL;
+    if (c->dtype != UBW_F16 && c->dtype != UBW_BF16 && c->dtype != UBW_E4M3) return UBW_EUNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return UBW_EUNSUPPORTED;
+    if (!page_size_ok(c->page_size)) return UBW_EUNSUPPORTED;
+    if (c->pages > (1 << 24) || c->kv_heads > 4096 || c->layers > 65536) return UBW_ERANGE;
+    if ((int64_t)c->pages * c->page_size > 0x7fffffff) return UBW_ERANGE;  // slots are int32
+    if (!aligned16(c->k) || !aligned16(c->v)) return UBW_EALIGN;
+    const int size = type_size(c->dtype);
+    int st = check_strides(c->k_stride, *c, size);
+    return st != UBW_OK ? st : check_strides(c->v_stride, *c, size);
+}
+
+// Rows of heads x head_dim values, ld elements apart.
+inline int check_rows(const void* p, int64_t ld, int64_t rows, int heads, int dim, int size) {
+    if (!p) return UBW_EINVAL;
+    if (rows > 1 && ld < (int64_t)heads * dim) return UBW_EINVAL;
+    if (ld < 0 || ld > ((int64_t)1 << 36)) return UBW_ERANGE;
+    if (!aligned16(p) || ((ld * size) & 15)) return UBW_EALIGN;
+    return UBW_OK;
+}
+
+// Workgroups that copy one page in every layer, and that compact one sequence.
+inline int64_t copy_grid(const ubw_kv_cache& c) {
+    return cdiv((int64_t)c.kv_heads * c.page_size * (c.head_dim * type_size(c.dtype) / 16), 256 * kCopyVecs) * c.layers;
+}
+inline int64_t compact_grid(const ubw_kv_cache& c) {
+    return cdiv((int64_t)c.layers * 2 * c.kv_heads * (c.head_dim * type_size(c.dtype) / 16), 256);
+}
+
+inline int check_pool(const ubw_page_pool* p) {
+    if (!p || !p->ref || !p->free_bits || !p->table || !p->held || !p->len || !p->status) return UBW_EINVAL;
+    if (p->pages < 1 || p->seqs < 1 || p->max_pages < 1) return UBW_EINVAL;
+    if (!page_size_ok(p->page_size)) return UBW_EUNSUPPORTED;
+    if (p->pages > (1 << 24) || p->seqs > UBW_MAX_SEQS || p->max_pages > (1 << 24)) return UBW_ERANGE;
+    if ((int64_t)p->max_pages * p->page_size > 0x7fffffff) return UBW_ERANGE;  // lengths are int32
+    return UBW_OK;
+}
+
+// ---- tree attention -------------------------------------------------------------------------
+// The rows of a (sequence, key/value head): row r is token r / G, query head h G + r % G (G =
+// heads / kv_heads). A workgroup takes a block of rows and a run of positions; its four waves are
+// row_waves groups of 16 tiles rows each, the others splitting the positions in units of 32.
+struct AttnTile {
+    int tiles;      // 16-row tiles a wave keeps (they share the loaded keys and values)
+    int row_waves;  // waves side by side over rows: 1, 2 or 4 (4 / row_waves over positions)
+};
+constexpr int kAttnItems = 1024;  // aimed-at number of pieces when contexts are split
+UBW_HD inline int attn_rows(AttnTile t) { return 16 * t.tiles * t.row_waves; }
+UBW_HD inline int attn_unit(AttnTile t) { return 32 * (4 / t.row_waves); }  // positions per step of the workgroup
+
+inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
+    if (head_dim == 256) {  // the sums of 256 dims take 64 registers per tile: one tile a wave
+        return AttnTile{1, max_rows <= 16 ? 1 : max_rows <= 32 ? 2 : 4};
+    }
+    if (max_rows <= 16) return AttnTile{1, 1};
+    if (max_rows <= 32) return AttnTile{2, 1};
+    if (max_rows <= 64) return AttnTile{2, 2};
+    return AttnTile{2, 4};
+}
+
+// How a batch is cut: sequence b has blocks_b row blocks of units_b units of positions for each
+// key/value head; a piece is one block over `chunk` units at most, a sequence's pieces of equal size
+// but for one unit. chunk is the smallest for which about kAttnItems pieces arise.
+UBW_HD inline int attn_chunk(int64_t total_units, int target) {
+    const int64_t c = (total_units + target - 1) / target;
+    return (int)(c < 1 ? 1 : c);
+}
+UBW_HD inline int attn_splits(int units, int chunk) { return units == 0 ? 0 : (units + chunk - 1) / chunk; }
+UBW_HD inline void attn_range(int units, int splits, int s, int* u0, int* u1) {
+    const int q = units / splits, r = units - q * splits;
+    *u0 = s * q + (s < r ? s : r);
+    *u1 = *u0 + q + (s < r ? 1 : 0);
+}
+// Most pieces of a batch: the sum over sequences of blocks kv ceil(units / chunk) is at most
+// total / chunk + batch blocks kv <= kAttnItems + batch blocks kv.
+inline int64_t attn_max_items(int batch, int64_t max_rows, int kv_heads, AttnTile t) {
+    return kAttnItems + (int64_t)batch * cdiv(max_rows, attn_rows(t)) * kv_heads;
+}
+// Scratch floats: each piece's rows (head_dim sums, then the running maximum and the sum of weights),
+// then the cut itself (units per piece, each sequence's first piece).
+inline int64_t attn_workspace_floats(int batch, int64_t max_rows, int kv_heads, int head_dim, AttnTile t) {
+    return attn_max_items(batch, max_rows, kv_heads, t) * attn_rows(t) * (head_dim + 2) + batch + 1;
+}
+
+}  // namespace cache
+}  // namespace ubw

@@ -1,0 +1,344 @@
+// Pages of the key/value cache: copying them, drawing kept tokens together, and the pool that shares
+// them out over sequences (who holds a page, what is free).
+//
+// The data calls move bytes and are bound by HBM (each byte read and written once) or, for a few
+// pages, by one launch. Both address 16-byte vectors: a row of a head is 4 to 32 of them, page sizes
+// are powers of two, so a vector's place in a page comes from shifts, and contiguous pages and pages
+// inside a larger row (token-major caches) run through the same code.
+//
+// The pool calls work on small integer tables and are bound by launch and memory latency. Their
+// results do not depend on timing: counts change by integer atomics (in any order the same), free
+// pages are a bit set, and pages are handed out by rank (prefix sums), never by arrival.
+#include "cache_internal.h"
+
+namespace ubw {
+namespace cache {
+namespace {
+
+constexpr uint32_t kNoPages = 1u, kNotServed = 2u;  // ubw_page_pool.status
+
+// ---- copying pages: blockIdx.y = (pair, layer) split in chunks of x, z = keys or values
+__global__ __launch_bounds__(256) void k_copy_pages(Pages c, int layers, int lrow, const int32_t* pairs, int vecs,
+                                                    int pieces) {
+    const uint32_t id = blockIdx.x;
+    const uint32_t piece = id % pieces, rest = id / pieces;
+    const uint32_t layer = rest % layers, i = rest / layers;
+    const int src = pairs[2 * i], dst = pairs[2 * i + 1];
+    if ((uint32_t)src >= (uint32_t)c.pages || (uint32_t)dst >= (uint32_t)c.pages || src == dst) return;
+    const bool v = blockIdx.y != 0;
+    const int64_t page = v ? c.v_page : c.k_page, head = v ? c.v_head : c.k_head;
+    const uint32_t row = v ? c.v_row : c.k_row;
+    char* base = (v ? c.v : c.k) + layer * (v ? c.v_layer : c.k_layer);
+    const char* from = base + src * page;
+    char* to = base + dst * page;
+    uint4 x[kCopyVecs];
+    int64_t off[kCopyVecs];
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j) {
+        const int n = (piece * kCopyVecs + j) * 256 + threadIdx.x;  // vector of the page
+        const int r = n >> lrow;
+        off[j] = n < vecs ? (r >> c.lps) * head + (int64_t)(r & ((1 << c.lps) - 1)) * row + (n & ((1 << lrow) - 1)) * 16 : -1;
+        if (off[j] >= 0) x[j] = *reinterpret_cast<const uint4*>(from + off[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kCopyVecs; ++j)
+        if (off[j] >= 0) *reinterpret_cast<uint4*>(to + off[j]) = x[j];
+}
+
+// ---- drawing kept tokens together: a thread owns one 16-byte column of a sequence's rows in one
+// layer and head and moves it row by row, eight at a time. A kept token's index is at least its
+// place, so the eight rows read lie at or behind the eight written and nothing is overwritten unread;
+// threads do not share columns.
+__global__ __launch_bounds__(256) void k_compact(Pages c, int layers, int lrow, const int32_t* table, int64_t ld_table,
+                                                 int table_cols, const int32_t* ctx_len, const int32_t* keep, int width) {
+    const int b = blockIdx.y;
+    const int ctx = ctx_len[b];
+    if (ctx < 0) return;
+    const uint32_t n = blockIdx.x * 256 + threadIdx.x;
+    const uint32_t r = n >> lrow;
+    const int h2 = (int)(r % (uint32_t)(2 * c.heads)), layer = (int)(r / (uint32_t)(2 * c.heads));
+    if (layer >= layers) return;
+    const bool v = h2 >= c.heads;
+    const int64_t page = v ? c.v_page : c.k_page;
+    const uint32_t row = v ? c.v_row : c.k_row;
+    char* base = (v ? c.v : c.k) + layer * (v ? c.v_layer : c.k_layer) + (h2 - (v ? c.heads : 0)) * (v ? c.v_head : c.k_head) +
+                 (n & ((1 << lrow) - 1)) * 16;
+    table += b * ld_table;
+    keep += (int64_t)b * width;
+    const auto at = [&](int64_t p) -> char* {  // the row of a position, or null
+        const int64_t col = p >> c.lps;
+        if (col >= table_cols) return nullptr;
+        const int pg = table[col];
+        if ((uint32_t)pg >= (uint32_t)c.pages) return nullptr;
+        return base + pg * page + (p & ((1 << c.lps) - 1)) * row;
+    };
+    int last = -1;
+    for (int i0 = 0; i0 < width; i0 += 8) {
+        uint4 x[8];
+        char* to[8];
+        bool ended = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            to[j] = nullptr;
+            if (ended || i0 + j >= width) continue;
+            const int k = keep[i0 + j];
+            if (k <= last) {  // negative or not ascending
+                ended = true;
+                continue;
+            }
+            last = k;
+            if (k == i0 + j) continue;  // in its place
+            const char* from = at((int64_t)ctx + k);
+            char* t = at((int64_t)ctx + i0 + j);
+            if (from && t) {
+                x[j] = *reinterpret_cast<const uint4*>(from);
+                to[j] = t;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (to[j]) *reinterpret_cast<uint4*>(to[j]) = x[j];
+        if (ended) return;
+    }
+}
+
+// ---- the pool
+__device__ inline int pages_for(int len, int lps) { return (int)(((int64_t)len + (1 << lps) - 1) >> lps); }
+
+__global__ __launch_bounds__(256) void k_pages_init(ubw_page_pool p) {
+    const int64_t stride = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (int64_t i = first; i < (int64_t)p.seqs * p.max_pages; i += stride) p.table[i] = -1;
+    for (int64_t i = first; i < p.pages; i += stride) p.ref[i] = 0;
+    for (int64_t i = first; i < (p.pages + 31) / 32; i += stride) {
+        const int64_t left = p.pages - i * 32;
+        p.free_bits[i] = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+    }
+    for (int64_t i = first; i < p.seqs; i += stride) p.held[i] = p.len[i] = 0;
+    if (first == 0) *p.status = 0;
+}
+
+// One workgroup per sequence.
+__global__ __launch_bounds__(256) void k_pages_trim(ubw_page_pool p, int lps, const int32_t* new_len) {
+    const int s = blockIdx.x;
+    const int n = new_len[s];
+    if (n < 0) return;
+    const int held = min(p.held[s], p.max_pages);
+    const int cut = pages_for(n, lps);
+    if (cut > held) {
+        if (threadIdx.x == 0) atomicOr(p.status, kNotServed);
+        return;
+    }
+    int32_t* row = p.table + (int64_t)s * p.max_pages;
+    for (int j = cut + (int)threadIdx.x; j < held; j += 256) {
+        const int pg = row[j];
+        row[j] = -1;
+        if ((uint32_t)pg < (uint32_t)p.pages && atomicSub(p.ref + pg, 1) == 1) atomicOr(p.free_bits + pg / 32, 1u << (pg & 31));
+    }
+    __syncthreads();  // every thread has read held
+    if (threadIdx.x == 0) {
+        p.held[s] = cut;
+        p.len[s] = n;
+    }
+}
+
+// One workgroup per sequence. A fork's parent is no fork of the same call, so no row that is read
+// here is written here.
+__global__ __launch_bounds__(256) void k_pages_fork(ubw_page_pool p, int lps, const int32_t* parents) {
+    const int s = blockIdx.x;
+    const int from = parents[s];
+    if (from < 0) return;
+    const bool known = from < p.seqs && from != s;
+    const int n = known ? p.len[from] : 0;
+    const int cut = pages_for(n, lps);
+    if (!known || parents[from] >= 0 || p.held[s] != 0 || n < 0 || cut > min(p.held[from], p.max_pages)) {
+        if (threadIdx.x == 0) atomicOr(p.status, kNotServed);
+        return;
+    }
+    const int32_t* src = p.table + (int64_t)from * p.max_pages;
+    int32_t* dst = p.table + (int64_t)s * p.max_pages;
+    for (int j = threadIdx.x; j < cut; j += 256) {
+        const int pg = src[j];
+        dst[j] = pg;
+        if ((uint32_t)pg < (uint32_t)p.pages) atomicAdd(p.ref + pg, 1);
+    }
+    __syncthreads();  // every thread has read held[s]
+    if (threadIdx.x == 0) {
+        p.held[s] = cut;
+        p.len[s] = n;
+    }
+}
+
+// The exclusive prefix sum over the workgroup's threads, in 64 bits (4096 sequences may ask for 2^24
+// pages each); *total gets the sum. `lds` has 17 words.
+__device__ inline int64_t wg_prefix(int64_t x, int64_t* lds, int64_t* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    int64_t y = x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t z = __shfl_up((long long)y, d);
+        if (lane >= d) y += z;
+    }
+    __syncthreads();  // lds may still be read from the call before
+    if (lane == 63) lds[wave] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int64_t sum = 0;
+        for (int w = 0; w < waves; ++w) {
+            const int64_t v = lds[w];
+            lds[w] = sum;
+            sum += v;
+        }
+        lds[16] = sum;
+    }
+    __syncthreads();
+    *total = lds[16];
+    return y - x + lds[wave];
+}
+
+// One workgroup: how many pages each sequence needs (a prefix sum over sequences), then the free
+// pages in order of their number (a prefix sum over the words of the bit set), the r-th free page
+// going to the sequence and place that r falls on.
+__global__ __launch_bounds__(1024) void k_pages_reserve(ubw_page_pool p, int lps, const int32_t* room, int32_t* pairs) {
+    __shared__ int before[UBW_MAX_SEQS + 1];  // pages needed by the sequences before s
+    __shared__ int64_t lds[17];
+    const int tid = threadIdx.x;
+    constexpr int kPer = UBW_MAX_SEQS / 1024;
+    int need[kPer], old[kPer], held[kPer];
+    int64_t mine = 0;
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int s = tid * kPer + u;
+        need[u] = held[u] = 0;
+        old[u] = -1;
+        if (s >= p.seqs) continue;
+        pairs[2 * s] = pairs[2 * s + 1] = -1;
+        const int r = room[s];
+        if (r <= 0) continue;
+        const int len = p.len[s], h = p.held[s];
+        const int64_t want = ((int64_t)len + r + (1 << lps) - 1) >> lps;
+        if (len < 0 || h < 0 || h > p.max_pages || want > p.max_pages || pages_for(len, lps) > h) {
+            bad = true;
+            continue;
+        }
+        const int at = len >> lps;
+        held[u] = h;
+        need[u] = max(0, (int)want - h);
+        if (at < h) {
+            const int pg = p.table[(int64_t)s * p.max_pages + at];
+            if ((uint32_t)pg < (uint32_t)p.pages && p.ref[pg] > 1) {
+                old[u] = pg;
+                ++need[u];
+            }
+        }
+        mine += need[u];
+    }
+    if (bad) atomicOr(p.status, kNotServed);
+    int64_t total;
+    int64_t first = wg_prefix(mine, lds, &total);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {  // read only where total <= pages: it fits
+        before[tid * kPer + u] = (int)first;
+        first += need[u];
+    }
+    if (tid == 1023) before[UBW_MAX_SEQS] = (int)first;
+    // free pages: this thread's words, and how many lie before them
+    const int words = (p.pages + 31) >> 5, per = (words + 1023) >> 10;
+    const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    int have = 0;
+    for (int w = w0; w < w1; ++w) have += __popc(p.free_bits[w]);
+    int64_t all;
+    int rank = (int)wg_prefix(have, lds, &all);  // its barriers also publish before[]
+    if (total > all) {
+        if (tid == 0) atomicOr(p.status, kNoPages);
+        return;
+    }
+    // hand out
+    for (int w = w0; w < w1 && rank < total; ++w) {
+        const uint32_t bits = p.free_bits[w];
+        uint32_t left = bits;
+        while (left && rank < total) {
+            const int pg = w * 32 + __ffs((int)left) - 1;
+            left &= left - 1;
+            int lo = 0, hi = UBW_MAX_SEQS;  // the last s with before[s] <= rank
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (before[mid] <= rank) lo = mid; else hi = mid;
+            }
+            const int s = lo;
+            int j = rank - before[s];
+            const int len = p.len[s], h = p.held[s];
+            int32_t* row = p.table + (int64_t)s * p.max_pages;
+            const int more = max(0, (int)(((int64_t)len + room[s] + (1 << lps) - 1) >> lps) - h);
+            const bool own_copy = before[s + 1] - before[s] > more;
+            if (own_copy && j == 0) {
+                pairs[2 * s + 1] = pg;  // its row is set below, once the old page is no longer read
+            } else {
+                row[h + j - (own_copy ? 1 : 0)] = pg;
+            }
+            p.ref[pg] = 1;
+            ++rank;
+        }
+        if (left != bits) p.free_bits[w] = left;
+    }
+    __threadfence();  // the words written here come before other threads' atomics on them
+    __syncthreads();  // pairs and the bit set are written; held and len are read no more
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int s = tid * kPer + u;
+        if (need[u] == 0) continue;
+        if (old[u] >= 0) {
+            pairs[2 * s] = old[u];
+            p.table[(int64_t)s * p.max_pages + (p.len[s] >> lps)] = pairs[2 * s + 1];
+            if (atomicSub(p.ref + old[u], 1) == 1) atomicOr(p.free_bits + old[u] / 32, 1u << (old[u] & 31));
+        }
+        p.held[s] = held[u] + need[u] - (old[u] >= 0 ? 1 : 0);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_copy_pages(const Pages& c, int layers, int page_size, int row_bytes, const int32_t* pairs, int count,
+                             hipStream_t s) {
+    const int lrow = log2_of(row_bytes / 16);
+    const int vecs = (c.heads * page_size) << lrow;
+    const int pieces = (int)cdiv(vecs, 256 * kCopyVecs);
+    const int64_t per_launch = kMaxGrid / ((int64_t)pieces * layers);  // at least 1 (checked by the caller)
+    for (int64_t i = 0; i < count; i += per_launch) {
+        const int64_t n = count - i < per_launch ? count - i : per_launch;
+        k_copy_pages<<<dim3((unsigned)(n * layers * pieces), 2), 256, 0, s>>>(c, layers, lrow, pairs + 2 * i, vecs, pieces);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_compact(const Pages& c, int layers, int row_bytes, const int32_t* table, int64_t ld_table,
+                          int table_cols, const int32_t* ctx_len, const int32_t* keep, int width, int batch,
+                          hipStream_t s) {
+    const int lrow = log2_of(row_bytes / 16);
+    const int64_t columns = ((int64_t)layers * 2 * c.heads) << lrow;
+    k_compact<<<dim3((unsigned)cdiv(columns, 256), batch), 256, 0, s>>>(c, layers, lrow, table, ld_table, table_cols,
+                                                                       ctx_len, keep, width);
+    return hipGetLastError();
+}
+
+hipError_t launch_pages_init(const ubw_page_pool& p, hipStream_t s) {
+    const int64_t n = (int64_t)p.seqs * p.max_pages > p.pages ? (int64_t)p.seqs * p.max_pages : p.pages;
+    const int64_t wgs = cdiv(n, 1024) < 2048 ? cdiv(n, 1024) : 2048;
+    k_pages_init<<<(unsigned)wgs, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+hipError_t launch_pages_trim(const ubw_page_pool& p, const int32_t* new_len, hipStream_t s) {
+    k_pages_trim<<<p.seqs, 256, 0, s>>>(p, log2_of(p.page_size), new_len);
+    return hipGetLastError();
+}
+hipError_t launch_pages_fork(const ubw_page_pool& p, const int32_t* parents, hipStream_t s) {
+    k_pages_fork<<<p.seqs, 256, 0, s>>>(p, log2_of(p.page_size), parents);
+    return hipGetLastError();
+}
+hipError_t launch_pages_reserve(const ubw_page_pool& p, const int32_t* room, int32_t* pairs, hipStream_t s) {
+    k_pages_reserve<<<1, 1024, 0, s>>>(p, log2_of(p.page_size), room, pairs);
+    return hipGetLastError();
+}
+
+}  // namespace cache
+}  // namespace ubw
