@@ -514,7 +514,7 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
  * are cut as above. tokens = 0 or batch = 0 enqueues nothing.
  * Errors: UBW_EINVAL (null, sizes, heads no multiple of kv_heads, scale not positive and finite),
  *         UBW_EUNSUPPORTED (types, head_dim, page_size), UBW_ERANGE (batch above UBW_MAX_SEQS,
- *         max_tree, strides, 2^24 pieces of work or more), UBW_EALIGN, UBW_ESIZE (workspace), UBW_EHIP.
+ *         max_tree, strides, 1024 query heads per key/value head, 2^24 pieces of work), UBW_EALIGN, UBW_ESIZE (workspace), UBW_EHIP.
  */
 int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_heads, int head_dim, size_t* out);
 int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,

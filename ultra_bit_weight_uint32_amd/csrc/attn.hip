@@ -5,30 +5,37 @@
 // the positions with a running maximum m and sum l per row:
 //     p_j = 2^(s_j log2 e - m),  l = sum p_j,  o = sum p_j v_j;   a larger m scales l and o down.
 //
-// A wave takes 32 positions at a time for 16 * MT rows, keys and values straight from memory into
-// registers (no LDS, no barrier in the loop):
-//   * S^T = K Q^T with v_mfma_f32_16x16x32: a lane loads 16-byte pieces of one key row, which are the
-//     A operand as they come; the result leaves lane (row, j) with the positions 4 j .. 4 j + 3 of both
-//     16-position halves.
+// A workgroup's waves lie R side by side over rows, MT tiles of 16 each, and T over positions. Keys and
+// values go from memory straight to LDS, 16 bytes a lane, without passing registers:
+//   * S^T = K Q^T with v_mfma_f32_16x16x32: keys lie in LDS as the A operand, in the order of the lanes
+//     that fetched them. The result leaves lane (row, j) with the positions 4 j .. 4 j + 3 of both
+//     16-position halves of a tile.
 //   * O^T = V^T P^T: those eight weights, packed to 16 bits, are the B operand as they are, if the
-//     operand's k index counts positions in that order. For A, lane (c, j) loads D / 16 consecutive
-//     dims c D / 16 .. of the same eight positions (16 lanes read a whole row) and eight v_perm per
-//     two dims turn the block: product e of a tile then has dim c D / 16 + e in its row c.
+//     operand's k index counts positions in that order. For A, transposing LDS reads give lane (dim, j)
+//     the same eight positions of its dim; value rows lie with their 16-byte columns exchanged by XOR so
+//     that these reads spread over the banks. 8-bit values are read so too and widened on the way.
 //   * m is not followed exactly: o is scaled only when a score passes m + 15 (a wave-uniform branch
 //     that long contexts take a few times), so the usual step has no cross-lane work at all, l is kept
 //     per lane, and p stays below 2^15, inside fp16. m starts 7 below the maximum, so that weights down
 //     to 2^-21 of the largest are normal fp16 numbers.
-// All loads are raw buffer loads through descriptors of 16 rows; a descriptor of size 0 stands for
-// rows that are not needed or on no valid page, so the loop loads one tile ahead without branches and
-// no table entry is ever trusted.
+// Descriptors cover 16 rows; one of size 0 stands for rows that are not needed or on no valid page, so
+// every step issues the same transfers, their count is waited for exactly, and no table entry is ever
+// trusted. Few rows (R = 1): each wave has tiles of its own and no barrier; with one tile, its keys make
+// room for the next ones while its values are used (two workgroups a CU with 128 dims in 16 bits, 8 decode
+// steps in flight; two tiles each, one workgroup a CU: 337 against 253 us for 1.3 GB). More rows: R waves
+// share each step, double-buffered, one barrier a step of 64 positions.
+// Nothing in the loop is a vector load the compiler knows of (the block table is read by the scalar
+// unit, the queries are waited for before): it would wait for it, and so for all transfers under way
+// (1.0 GB at 128 rows: 226 us with such waits, 170 without).
 //
 // Split over workgroups: the pieces (sequence, head, row block, run of positions) are cut on the
-// device from the lengths, about kAttnItems of equal size, and taken by a grid of resident workgroups;
-// a piece that is not a whole sequence leaves o, m, l in the workspace and k_join adds them up in order.
+// device from the lengths, of equal size, and taken by a grid of resident workgroups; a piece that is not
+// a whole sequence leaves o, m, l in the workspace and k_join adds them up in order. Few rows take about
+// three pieces a workgroup (ragged batches: 249 against 269 us), many rows one (their sums are large:
+// 170 against 198 us).
 //
-// Bound: HBM where G n is small (2 (L + n) D values per head read once against 4 G n D operations per
-// position); from about 64 rows on the vector unit (exponentials, the turning of V, packing) beside
-// the matrix cores.
+// Bound: HBM up to about 128 rows (5.0 to 5.3 TB/s of keys and values, where a plain streaming read of
+// this card reaches 6.4); beyond, the vector unit beside the matrix cores.
 #include "cache_internal.h"
 
 namespace ubw {
@@ -82,6 +89,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1e30f;     // m of a row that has seen nothing: 2^(-inf - kLow) = 0
 constexpr float kShift = 7.f, kSlack = 8.f;
 
+constexpr int kCus = 256;
+
+// Words that no kernel running beside this one writes, read by the scalar unit. (As vector loads they
+// would be waited for behind all transfers under way.)
+typedef const __attribute__((address_space(4))) int32_t ScalarWord;
+__device__ inline ScalarWord* scalar_words(const int32_t* p) { return (ScalarWord*)(uintptr_t)p; }
+
 // ---- what a piece is
 struct Seq {
     int ctx, n, q0;  // context, tokens, first row of q
@@ -102,11 +116,10 @@ __device__ inline int positions(const AttnArgs& a, const Seq& s) {
 struct Plan {
     int units, blocks, splits;
 };
-template <int RB, int U>
-__device__ inline Plan plan_of(const AttnArgs& a, const Seq& s, int chunk) {
+__device__ inline Plan plan_of(const AttnArgs& a, const Seq& s, int rb, int chunk) {
     Plan p;
-    p.blocks = s.n > 0 ? (s.n * a.group + RB - 1) / RB : 0;
-    p.units = s.n > 0 ? max(1, (int)(((int64_t)positions(a, s) + U - 1) / U)) : 0;
+    p.blocks = s.n > 0 ? (s.n * a.group + rb - 1) / rb : 0;
+    p.units = s.n > 0 ? max(1, (int)(((int64_t)positions(a, s) + kAttnUnit - 1) / kAttnUnit)) : 0;
     p.splits = chunk > 0 ? attn_splits(p.units, chunk) : min(p.units, 1);
     return p;
 }
@@ -120,33 +133,43 @@ __device__ inline uint32_t four_seen(uint64_t mask, int d) {
     return x > 67 ? 0u : (uint32_t)b & 15u;
 }
 
-// Sum over the workgroup's 256 threads (every thread gets it). `lds`: 4 words.
+// Sum over the workgroup's NT threads (every thread gets it). `lds`: 4 words.
+template <int NT>
 __device__ inline int64_t wg_sum(int64_t x, int64_t* lds) {
 #pragma unroll
     for (int d = 32; d; d >>= 1) x += __shfl_xor((long long)x, d);
+    __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = lds[0] + lds[1] + lds[2] + lds[3];
-    __syncthreads();
-    return x;
+    int64_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) sum += lds[w];
+    return sum;
 }
 
-// Cuts the batch: units per piece, and in pre[b] the number of pieces of the sequences before b.
-template <int RB, int U>
-__device__ inline int cut_batch(const AttnArgs& a, int* pre, int64_t* lds) {
+// Cuts the batch: units per piece (the least for which the pieces do not pass the target by more than
+// the sequences that cannot be joined make them), and in pre[b] the pieces of the sequences before b.
+template <int NT>
+__device__ inline int cut_batch(const AttnArgs& a, int rb, int* pre, int64_t* lds) {
     const int tid = threadIdx.x;
-    const int per = (a.batch + 255) >> 8;
+    const int per = (a.batch + NT - 1) / NT;
     const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
     int64_t units = 0;
     for (int b = b0; b < b1; ++b) {
-        const Plan p = plan_of<RB, U>(a, seq_of(a, b), 0);
+        const Plan p = plan_of(a, seq_of(a, b), rb, 0);
         units += (int64_t)p.units * p.blocks;
     }
-    const int chunk = attn_chunk(wg_sum(units, lds) * a.c.heads, a.target);
+    int chunk = attn_chunk(wg_sum<NT>(units, lds) * a.c.heads, a.target);
     int mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Plan p = plan_of<RB, U>(a, seq_of(a, b), chunk);
-        mine += p.splits * p.blocks * a.c.heads;
+    for (int step = 0;; ++step) {
+        mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Plan p = plan_of(a, seq_of(a, b), rb, chunk);
+            mine += p.splits * p.blocks * a.c.heads;
+        }
+        const int64_t pieces = wg_sum<NT>(mine, lds);
+        if (step == 4 || pieces <= a.target) break;
+        chunk = attn_larger_chunk(chunk, pieces, a.target);
     }
     int y = mine;
 #pragma unroll
@@ -155,16 +178,17 @@ __device__ inline int cut_batch(const AttnArgs& a, int* pre, int64_t* lds) {
         if ((tid & 63) >= d) y += z;
     }
     int* sums = reinterpret_cast<int*>(lds);
+    __syncthreads();
     if ((tid & 63) == 63) sums[tid >> 6] = y;
     __syncthreads();
     int first = y - mine;
     for (int w = 0; w < (tid >> 6); ++w) first += sums[w];
     for (int b = b0; b < b1; ++b) {
-        const Plan p = plan_of<RB, U>(a, seq_of(a, b), chunk);
+        const Plan p = plan_of(a, seq_of(a, b), rb, chunk);
         pre[b] = first;
         first += p.splits * p.blocks * a.c.heads;
     }
-    if (tid == 255) pre[a.batch] = first;
+    if (tid == NT - 1) pre[a.batch] = first;
     __syncthreads();
     return chunk;
 }
@@ -180,82 +204,134 @@ __device__ inline Rsrc rows16(const char* p, uint32_t bytes) {
                                              0x00020000);
 }
 
-// One tile's keys and values in registers, as loaded.
+// ---- a tile in LDS: 32 positions of one key/value head, as 1 KiB pieces of 64 lanes x 16 bytes
 template <bool FP8, int D>
-struct Tile {
-    static constexpr int NV = D / 16;                  // dims a lane has of a value row
-    static constexpr int KL = FP8 ? D / 64 : D / 32;   // 16-byte pieces of a key row per lane
-    static constexpr int VB = FP8 ? NV : 2 * NV;       // bytes of a value row per lane
-    static constexpr int VW = VB / 4;
-    u32x4 k[2][KL];
-    uint32_t v[8][VW];
-    __device__ void load_k(int sub, Rsrc r, uint32_t off) {  // off: the lane's row and 16-byte column
-#pragma unroll
-        for (int s = 0; s < KL; ++s) {
-            const auto x = __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + s * 64), 0, 0);
-            k[sub][s] = __builtin_bit_cast(u32x4, x);
-        }
-    }
-    __device__ void load_v(int sub, Rsrc r, uint32_t off, uint32_t row) {  // off: row 4 j, dims of c
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t o = off + i * row;
-            uint32_t(&w)[VW] = v[sub * 4 + i];
-            if constexpr (VB == 4) {
-                w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)o, 0, 0);
-            } else if constexpr (VB == 8) {
-                const auto x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)o, 0, 0));
-                w[0] = x.x;
-                w[1] = x.y;
-            } else {
-#pragma unroll
-                for (int q = 0; q < VB / 16; ++q) {
-                    const auto x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(o + q * 16), 0, 0));
-                    w[4 * q] = x.x;
-                    w[4 * q + 1] = x.y;
-                    w[4 * q + 2] = x.z;
-                    w[4 * q + 3] = x.w;
-                }
-            }
-        }
-    }
+struct Layout {
+    static constexpr int kElem = FP8 ? 1 : 2, kRowB = D * kElem;
+    static constexpr int KL = kRowB / 64;            // pieces of 16 key rows
+    static constexpr int P = kRowB / 16;             // 16-byte columns of a value row
+    static constexpr int RP = 64 / P;                // value rows in a piece
+    static constexpr int CK = 2 * KL, CV = 32 / RP;  // pieces of keys, of values
+    static constexpr int kBytes = 64 * kRowB;
+    // Keys lie as the A operand of S^T = K Q^T takes them: piece (half, s), lane (c, j) = row c, bytes
+    // 64 s + 16 j .. Values lie row by row, the 16-byte columns of row t exchanged by XOR with this, so
+    // that the 16 or 32 rows a transposing read touches spread over all banks.
+    static __device__ constexpr int mix(int t) { return (P >= 16 ? t : P == 8 ? t >> 1 : t >> 2) & (P >= 16 ? 15 : P - 1); }
 };
 
-template <typename TQ, bool FP8, int D, int MT, int RW>
-__global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
+// 16 bytes a lane from memory straight to LDS at `lds` + 16 lane. The compiler does not see the
+// transfer: waits are placed by hand.
+template <int OFF>
+__device__ inline void to_lds(Rsrc r, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds" ::"s"(lds), "v"(off), "s"(r),
+                 "n"(OFF)
+                 : "memory");
+}
+template <int N>
+__device__ inline void wait_loads() {  // all but the newest N transfers have arrived
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ inline void wait_and_meet() {  // LDS reads done, then the workgroup's barrier
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+template <typename T>
+__device__ inline T* lds_at(uint32_t at) {
+    return (T*)(__attribute__((address_space(3))) T*)(uintptr_t)at;
+}
+
+// The elements of a word that are infinite or NaN (e4m3: NaN), as a mask.
+template <typename TQ, bool FP8>
+__device__ inline uint32_t not_finite(uint32_t w) {
+    if constexpr (FP8) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) m |= ((w >> k) & 0x7f) == 0x7f ? 0xffu << k : 0u;
+        return m;
+    } else {
+        constexpr uint32_t e = Half<TQ>::kExp;
+        return ((w & e) == e ? 0xffffu : 0u) | (((w >> 16) & e) == e ? 0xffff0000u : 0u);
+    }
+}
+
+constexpr int kW = 2;
+// MT row tiles a wave, R waves side by side over rows, T over positions, NS tiles of 32 positions a
+// step, NB steps in LDS for each of the T.
+template <bool FP8, int D, int MT, int R, int T, int NS, int NB>
+struct Cfg {
+    static constexpr int kThreads = 64 * R * T, RB = 16 * MT * R;
+    static constexpr int kTiles = T * NB * NS * Layout<FP8, D>::kBytes;
+    static constexpr int kJoin = (T - 1) * RB * (D + 4) * 4;  // laid over the tiles
+    static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
+    // workgroups per CU: by LDS, and waves per SIMD by registers
+    static constexpr int kFit = (160 * 1024 - 512) / (kLds + 8 * T * RB + 1024);
+    static constexpr int kWaves = D * MT > 256 ? 1 : D * MT == 256 ? (NS == 1 ? 3 : kW) : 3;
+    static constexpr int kMost = kWaves * 256 / kThreads;
+    static constexpr int kPerCu = kFit < kMost ? kFit : kMost;
+    static constexpr int kSimd = kPerCu * kThreads / 256 < 1 ? 1 : kPerCu * kThreads / 256;
+};
+
+template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB>
+__global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8, D, MT, R, T, NS, NB>::kSimd)) void k_attn(AttnArgs a) {
     using H = Half<TQ>;
-    using T = Tile<FP8, D>;
-    constexpr int NV = D / 16, KS = D / 32, TW = 4 / RW, RB = 16 * MT * RW, U = 32 * TW;
-    constexpr int kRow = D + 4;  // LDS row of o, in floats
-    extern __shared__ char lds_raw[];
+    using L = Layout<FP8, D>;
+    using C = Cfg<FP8, D, MT, R, T, NS, NB>;
+    constexpr int NE = D / 16, KS = D / 32, RB = C::RB, U = kAttnUnit, STEP = 32 * NS * T;
+    constexpr int NC = (L::CK + L::CV) / R;  // transfers of a wave per tile
+    constexpr int NP = 2 * NS * (R > 1 ? T : 1);  // pages of a step that a wave knows
+    constexpr int kRow = D + 4;              // LDS row of o, in floats
+    static_assert((L::CK + L::CV) % R == 0, "pieces of a tile are shared out evenly");
+    static_assert(R > 1 ? NB == 2 : NS == 1, "shared steps are double-buffered, private ones have one tile");
+    extern __shared__ int pre[];  // [batch + 1], with a split
     __shared__ int64_t lds64[4];
-    __shared__ float ml[TW][RB][2];
-    float* o_lds = reinterpret_cast<float*>(lds_raw);                             // [TW - 1][RB][kRow]
-    int* pre = reinterpret_cast<int*>(lds_raw + (size_t)(TW - 1) * RB * kRow * 4);  // [batch + 1], with a split
+    __shared__ float ml[T][RB][2];
+    __shared__ int odd[2];  // of this piece and the next: values of the tree that are not finite were met
+    if (threadIdx.x == 0) odd[0] = 0;
+    int turn = 0;
+    __shared__ __align__(1024) char buf[C::kLds];
+    const uint32_t buf0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)buf;
+    float* o_lds = reinterpret_cast<float*>(buf);
 
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rw = wave % RW, tw = wave / RW;
+    const int rw = wave % R, tw = wave / R;
     const float c2 = a.scale * kLog2e;
 
     int chunk = 0, items;
     const int blocks_max = (a.max_tree * a.group + RB - 1) / RB;
     if (a.target > 0) {
-        chunk = cut_batch<RB, U>(a, pre, lds64);
-        items = pre[a.batch];
+        chunk = cut_batch<C::kThreads>(a, RB, pre, lds64);
+        items = __builtin_amdgcn_readfirstlane(pre[a.batch]);
         if (blockIdx.x == 0) {  // for k_join
             int* head = reinterpret_cast<int*>(a.ws + a.max_items * RB * (D + 2));
-            for (int b = threadIdx.x; b < a.batch; b += 256) head[1 + b] = pre[b];
+            for (int b = threadIdx.x; b < a.batch; b += C::kThreads) head[1 + b] = pre[b];
             if (threadIdx.x == 0) head[0] = chunk;
         }
     } else {
         items = a.batch * a.c.heads * blocks_max;
     }
 
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    // this lane's part of the transfers and reads, in bytes
+    const uint32_t tile0 = buf0 + tw * (NB * NS * L::kBytes);
+    const uint32_t koff = c * a.c.k_row + j * 16;
+    const int vt = lane / L::P, vp = lane % L::P;           // row and column of a value piece
+    const int q4 = c >> 2, q2 = c >> 1;                     // a transposing read: rows by fours, by eights
+    const int vrow = FP8 ? 4 * j + (q2 & 3) + (q2 & 4) * 4 : 4 * j + q4;
+    const uint32_t vread = L::CK * 1024 + vrow * L::kRowB +
+                           (FP8 ? L::mix(vrow) * 16 + (c & 1) * 8
+                                : (((c >> 1) & 1) ^ (L::mix(vrow) & 1)) * 16 + (c & 1) * 8 + (L::mix(vrow) & ~1) * 16);
+
+    // Workgroups go to the eight XCDs in turn; each XCD takes a contiguous eighth of the pieces, so that
+    // the row blocks over the same keys and values, neighbours in the list, meet in one L2.
+    const int eighth = (items + 7) >> 3;
+    for (int it = blockIdx.x; it < 8 * eighth; it += gridDim.x) {
+        const int item = (it & 7) * eighth + (it >> 3);
+        if (item >= items) continue;
         int b, h, blk, split;
         Seq s;
         Plan p;
+        if (threadIdx.x == 0) odd[turn ^ 1] = 0;
         if (a.target > 0) {
             int lo = 0, hi = a.batch;  // the last b with pre[b] <= item
             while (hi - lo > 1) {
@@ -264,7 +340,7 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
             }
             b = __builtin_amdgcn_readfirstlane(lo);
             s = seq_of(a, b);
-            p = plan_of<RB, U>(a, s, chunk);
+            p = plan_of(a, s, RB, chunk);
             int r = item - __builtin_amdgcn_readfirstlane(pre[b]);
             blk = r % p.blocks;
             r /= p.blocks;
@@ -276,7 +352,7 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
             h = r % a.c.heads;
             b = r / a.c.heads;
             s = seq_of(a, b);
-            p = plan_of<RB, U>(a, s, 0);
+            p = plan_of(a, s, RB, 0);
             split = 0;
             if (blk >= p.blocks) continue;
         }
@@ -285,15 +361,68 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
         attn_range(p.units, p.splits, split, &u0, &u1);
         const int r0 = blk * RB + rw * 16 * MT + c;  // this lane's row of tile 0
 
-        // queries: the B operand of S^T = K Q^T (8-bit keys come 16 dims a lane, so 32-dim steps take
-        // the dims 64 s + 16 j + 8 half ..)
+        const char* kb = a.c.k + h * a.c.k_head;
+        const char* vb = a.c.v + h * a.c.v_head;
+        const auto* table = scalar_words(a.table + b * a.ld_table);
+        const int lps = a.c.lps, pmask = (1 << lps) - 1;
+        const int t_end = min(u1 * U, len);
+        const auto page_at = [&](int t) -> int {  // page of position t, -1: none
+            if (t >= t_end) return -1;
+            const int pg = table[t >> lps];
+            return (uint32_t)pg < (uint32_t)a.c.pages ? pg : -1;
+        };
+        // Pages of a step's positions, sixteen at a time: of this wave's tile, or with R > 1 of all tiles of the
+        // step (whether the waves meet to clean them is decided alike in all).
+        struct Pg {
+            int p[NP];
+        };
+        const auto pages_at = [&](int t) {  // t: first position of the step, or of the tile
+            Pg g;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) g.p[i] = page_at(t + 16 * i);
+            return g;
+        };
+        const auto own = [&](const Pg& g, int sub) {  // of sixteen positions of this wave's tiles
+            return R > 1 && T > 1 && tw == 1 ? g.p[(2 * NS) % NP + sub] : g.p[sub];
+        };
+        // The transfers of this wave for the step at t, those from first to last of each tile; rows that are not
+        // needed or on no page arrive as zeros.
+        const auto fetch = [&](int t, const Pg& pg, uint32_t at, int first, int last) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const int ch = i * R + rw;
+                    const uint32_t to = at + n * L::kBytes + ch * 1024;
+                    if (i < first || i >= last) continue;
+                    if (ch < L::CK) {
+                        const int sub = ch / L::KL, piece = ch % L::KL;
+                        const int page = sub ? own(pg, 2 * n + 1) : own(pg, 2 * n);
+                        to_lds<0>(rows16(kb + (page < 0 ? 0 : page) * a.c.k_page + (int64_t)((t + 32 * n + 16 * sub) & pmask) * a.c.k_row + piece * 64,
+                                         page < 0 ? 0u : 16 * a.c.k_row - piece * 64), koff, to);
+                    } else {
+                        const int row = (ch - L::CK) * L::RP, sub = row >> 4;  // of the tile
+                        const int page = sub ? own(pg, 2 * n + 1) : own(pg, 2 * n);
+                        const uint32_t off = (uint32_t)vt * a.c.v_row + (uint32_t)((vp ^ L::mix((row + vt) & 15)) * 16);
+                        to_lds<0>(rows16(vb + (page < 0 ? 0 : page) * a.c.v_page + (int64_t)((t + 32 * n + row) & pmask) * a.c.v_row,
+                                         page < 0 ? 0u : L::RP * a.c.v_row), off, to);
+                    }
+                }
+        };
+        int t0 = u0 * U + 32 * NS * tw;
+        const int base = R > 1 ? u0 * U : t0;
+        Pg pa = pages_at(base), pb = pages_at(base + STEP), pc = pages_at(base + 2 * STEP), pd = pages_at(base + 3 * STEP);
+        fetch(t0, pa, tile0, 0, NC);
+        if constexpr (R == 1 && NB == 2) fetch(t0 + STEP, pb, tile0 + L::kBytes, 0, NC);
+
+        // queries: the B operand of S^T (8-bit keys come 16 dims a lane, so 32-dim steps take the dims
+        // 64 s + 16 j + 8 half ..)
         u32x4 q[MT][KS];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int r = r0 + 16 * m;
             const int t = r / a.group, g = r - t * a.group;
-            const char* at = static_cast<const char*>(a.q) +
-                             ((int64_t)(s.q0 + t) * a.ldq + (int64_t)(h * a.group + g) * D) * 2;
+            const char* at = static_cast<const char*>(a.q) + ((int64_t)(s.q0 + t) * a.ldq + (int64_t)(h * a.group + g) * D) * 2;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 const int d = FP8 ? (ks >> 1) * 64 + j * 16 + (ks & 1) * 8 : ks * 32 + j * 8;
@@ -307,241 +436,226 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
         }
         const float cc = c2 * ks_scale;
 
-        const char* kb = a.c.k + h * a.c.k_head;
-        const char* vb = a.c.v + h * a.c.v_head;
-        const int32_t* table = a.table + b * a.ld_table;
-        const uint32_t koff = c * a.c.k_row + j * 16;
-        const uint32_t voff = 4 * j * a.c.v_row + c * T::VB;
-        const int lps = a.c.lps, pmask = (1 << lps) - 1;
-        const int t_end = min(u1 * U, len);
-        const auto page_at = [&](int t) -> int {  // page of position t, -1: none
-            if (t >= t_end) return -1;
-            const int pg = table[t >> lps];
-            return (uint32_t)pg < (uint32_t)a.c.pages ? pg : -1;
-        };
-        T x;
-        const auto load_k = [&](int t, const int (&pg)[2]) {
+        // The compiler waits for the queries here, once, instead of at their first use in the loop, where it
+        // would wait for all transfers under way as well.
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-                x.load_k(sub, rows16(kb + (pg[sub] < 0 ? 0 : pg[sub]) * a.c.k_page + (int64_t)((t + 16 * sub) & pmask) * a.c.k_row,
-                                     pg[sub] < 0 ? 0u : 16 * a.c.k_row), koff);
-        };
-        const auto load_v = [&](int t, const int (&pg)[2]) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-                x.load_v(sub, rows16(vb + (pg[sub] < 0 ? 0 : pg[sub]) * a.c.v_page + (int64_t)((t + 16 * sub) & pmask) * a.c.v_row,
-                                     pg[sub] < 0 ? 0u : 16 * a.c.v_row), voff, a.c.v_row);
-        };
+            for (int ks = 0; ks < KS; ++ks) asm volatile("" : "+v"(q[m][ks]));
 
-        f32x4 o[MT][NV];
+        f32x4 o[MT][NE];
         float mx[MT], l[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             mx[m] = kLow;
             l[m] = 0.f;
 #pragma unroll
-            for (int e = 0; e < NV; ++e) o[m][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int e = 0; e < NE; ++e) o[m][e] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        int t0 = u0 * U + 32 * tw;
-        int pg[2] = {page_at(t0), page_at(t0 + 16)};
-        load_k(t0, pg);
-        load_v(t0, pg);
-        int pn[2] = {page_at(t0 + U), page_at(t0 + U + 16)};
-        for (; t0 < t_end; t0 += U) {
-            // scores of 32 positions
-            f32x4 sc[MT][2];
+        // The values of 16 dims turned: lane (c, j) gets dim 16 e + c of the positions 4 j .. of both halves.
+        const auto turned = [&](uint32_t at, int e) -> u32x4 {
+            if constexpr (FP8) {
+                const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (__attribute__((address_space(3))) i32x2*)(uintptr_t)(at + (vread ^ (uint32_t)(e * 16))));
+                return u32x4{H::from8(w.x, false), H::from8(w.x, true), H::from8(w.y, false), H::from8(w.y, true)};
+            } else {
+                const uint32_t x = at + (vread ^ (uint32_t)(e * 32));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(uintptr_t)x);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4*)(uintptr_t)(x + 16 * L::kRowB));
+                const u32x2 y = __builtin_bit_cast(u32x2, lo), z = __builtin_bit_cast(u32x2, hi);
+                return u32x4{y.x, y.y, z.x, z.y};
+            }
+        };
+        const auto scores = [&](uint32_t at, f32x4 (&sc)[MT][2 * NS]) {
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+            for (int sub = 0; sub < 2 * NS; ++sub) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) sc[m][sub] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t from = at + (sub >> 1) * L::kBytes + (sub & 1) * L::KL * 1024 + lane * 16;
                     u32x4 kk;
                     if constexpr (FP8) {
-                        const u32x4 w = x.k[sub][ks >> 1];
+                        const u32x4 w = *lds_at<const u32x4>(from + (ks >> 1) * 1024);
                         const uint32_t lo = (ks & 1) ? w.z : w.x, hi = (ks & 1) ? w.w : w.y;
                         kk = u32x4{H::from8(lo, false), H::from8(lo, true), H::from8(hi, false), H::from8(hi, true)};
                     } else {
-                        kk = x.k[sub][ks];
+                        kk = *lds_at<const u32x4>(from + ks * 1024);
                     }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) sc[m][sub] = H::mfma(kk, q[m][ks], sc[m][sub]);
                 }
             }
-            load_k(t0 + U, pn);
-
-            const bool whole = t0 + 32 <= s.ctx && t0 + 32 <= t_end && pg[0] >= 0 && pg[1] >= 0;
-            uint32_t sees[MT];  // bit 4 sub + i: position t0 + 16 sub + 4 j + i (only where !whole)
+        };
+        // Hides from row tile m the positions of the step at t0 that it does not see.
+        const auto hide = [&](int m, f32x4 (&sc)[2 * NS]) {
+            const int t = min(r0 + 16 * m, rows - 1) / a.group;
+            const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
+#pragma unroll
+            for (int sub = 0; sub < 2 * NS; ++sub) {
+                const int x = t0 + 16 * sub + 4 * j;
+                const uint32_t there = own(pa, sub) < 0 ? 0u : (1u << min(max(t_end - x, 0), 4)) - 1;
+                const uint32_t sees = four_seen(mask, x - s.ctx) & there;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[sub][k] = (sees >> k) & 1 ? sc[sub][k] : -INFINITY;
+            }
+        };
+        // Values that are no part of a sum must not reach it even as 0 * NaN: rows of the tile behind the
+        // sequence or on no page become zeros in LDS, and so do values of the tree that are not finite (set
+        // aside: `odd` asks for them at the end).
+        const auto clean = [&](uint32_t at) {
+            bool found = false;
+            for (int n = rw * 64 + lane; n < 32 * NS * L::P; n += 64 * R) {
+                const int row = n / L::P, x = t0 + row;
+                u32x4* w = lds_at<u32x4>(at + (row >> 5) * L::kBytes + L::CK * 1024 + (n % (32 * L::P)) * 16);
+                bool none = x >= t_end;
+#pragma unroll
+                for (int k = 0; k < 2 * NS; ++k) none |= row >> 4 == k && own(pa, k) < 0;
+                const bool tree = x >= s.ctx;
+                u32x4 y = *w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t nf = not_finite<TQ, FP8>(y[k]);
+                    found |= tree && !none && nf != 0;
+                    y[k] = none ? 0u : tree ? y[k] & ~nf : y[k];
+                }
+                if (none || tree) *w = y;
+            }
+            if (found) odd[turn] = 1;
+        };
+        // A tile at LDS address `at`.
+        const auto step = [&](uint32_t at, bool whole) {
+            f32x4 sc[MT][2 * NS];
+            scores(at, sc);
+            if constexpr (NB == 1) {  // one tile: its keys make room for the next ones, then its values
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                fetch(t0 + STEP, pb, at, 0, NC / 2);
+                wait_loads<NC / 2>();
+            }
             if (!whole) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int r = r0 + 16 * m;
-                    const int t = min(r, rows - 1) / a.group;
-                    const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
-                    sees[m] = 0;
-#pragma unroll
-                    for (int sub = 0; sub < 2; ++sub) {
-                        const int at = t0 + 16 * sub + 4 * j;
-                        const uint32_t there = pg[sub] < 0 ? 0u : (1u << min(max(t_end - at, 0), 4)) - 1;
-                        sees[m] |= (four_seen(mask, at - s.ctx) & there) << (4 * sub);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sc[m][k >> 2][k & 3] = (sees[m] >> k) & 1 ? sc[m][k >> 2][k & 3] : -INFINITY;
-                }
+                for (int m = 0; m < MT; ++m) hide(m, sc[m]);
+                if constexpr (R == 1) clean(at);
             }
-
-            // weights
+            float top[MT];
             bool passed = false;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                float top = sc[m][0][0];
+                top[m] = sc[m][0][0];
 #pragma unroll
-                for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[m][i >> 2][i & 3]);
-                passed |= fmaf(top, cc, -mx[m]) > kShift + kSlack;
+                for (int k = 1; k < 8 * NS; ++k) top[m] = fmaxf(top[m], sc[m][k >> 2][k & 3]);
+                passed |= fmaf(top[m], cc, -mx[m]) > kShift + kSlack;
             }
             if (__any(passed)) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    float top = sc[m][0][0];
-#pragma unroll
-                    for (int i = 1; i < 8; ++i) top = fmaxf(top, sc[m][i >> 2][i & 3]);
-                    top = fmaxf(top, __shfl_xor(top, 16));
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    const float to = fmaxf(mx[m], fmaf(top, cc, -kShift));
+                    float x = fmaxf(top[m], __shfl_xor(top[m], 16));
+                    x = fmaxf(x, __shfl_xor(x, 32));
+                    const float to = fmaxf(mx[m], fmaf(x, cc, -kShift));
                     const float f = __builtin_amdgcn_exp2f(mx[m] - to);
                     mx[m] = to;
                     l[m] *= f;
 #pragma unroll
-                    for (int e = 0; e < NV; ++e) o[m][e] *= f;
+                    for (int e = 0; e < NE; ++e) o[m][e] *= f;
                 }
             }
-            u32x4 pf[MT];
-            float pr[MT][8];
+            u32x4 pf[MT][NS];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    pr[m][i] = __builtin_amdgcn_exp2f(fmaf(sc[m][i >> 2][i & 3], cc, -mx[m]));
-                    l[m] += pr[m][i];
-                }
-                pf[m] = u32x4{pack<TQ>(pr[m][0], pr[m][1]), pack<TQ>(pr[m][2], pr[m][3]), pack<TQ>(pr[m][4], pr[m][5]),
-                              pack<TQ>(pr[m][6], pr[m][7])};
-            }
-
-            // values in 16 bits: w[position][dim pair]
-            uint32_t w[8][NV / 2];
+                for (int n = 0; n < NS; ++n) {
+                    float pr[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int e = 0; e < NV / 2; ++e) {
-                    if constexpr (FP8)
-                        w[k][e] = H::from8(x.v[k][e >> 1], e & 1);
-                    else
-                        w[k][e] = x.v[k][e];
-                }
-            if (!whole) {
-                // Rows behind the sequence must not reach the sums even as 0 * NaN. Values of the tree
-                // that are not finite are taken out of the product and added by hand to the rows that see
-                // them, so that the others stay clean.
-                bool odd = false;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int at = t0 + 16 * (k >> 2) + 4 * j + (k & 3);
-                    const bool none = at >= t_end, tree = at >= s.ctx;
-#pragma unroll
-                    for (int e = 0; e < NV / 2; ++e) {
-                        w[k][e] = none ? 0u : w[k][e];
-                        const bool lo = tree && (w[k][e] & H::kExp) == H::kExp;
-                        const bool hi = tree && ((w[k][e] >> 16) & H::kExp) == H::kExp;
-                        odd |= lo || hi;
-                        w[k][e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0x0000ffffu : ~0u);
+                    for (int k = 0; k < 8; ++k) {
+                        pr[k] = __builtin_amdgcn_exp2f(fmaf(sc[m][2 * n + (k >> 2)][k & 3], cc, -mx[m]));
+                        l[m] += pr[k];
                     }
+                    pf[m][n] = u32x4{pack<TQ>(pr[0], pr[1]), pack<TQ>(pr[2], pr[3]), pack<TQ>(pr[4], pr[5]), pack<TQ>(pr[6], pr[7])};
                 }
-                if (__any(odd)) {
-                    for (int k = 0; k < 32; ++k) {  // position t0 + k
-                        const int at = t0 + k, sub = k >> 4, slot = 4 * sub + (k & 3), from = ((k >> 2) & 3) * 16 + c;
-                        if (at < s.ctx || at >= t_end || pg[sub] < 0) continue;
-                        const char* row = vb + (int64_t)pg[sub] * a.c.v_page + (int64_t)(at & pmask) * a.c.v_row;
-                        float pk[MT];
-                        bool see[MT];
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            float v = pr[m][0];
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
-                            for (int i = 1; i < 8; ++i) v = slot == i ? pr[m][i] : v;
-                            pk[m] = __shfl(v, from);
-                            see[m] = (__shfl((int)sees[m], from) >> slot) & 1;
-                        }
+                for (int e = 0; e < NE; ++e) {
+                    const u32x4 v = turned(at + n * L::kBytes, e);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                    for (int m = 0; m < MT; ++m) o[m][e] = H::mfma(v, pf[m][n], o[m][e]);
+                }
+        };
+        uint32_t at = tile0;
+        for (int tb = base; tb < t_end; tb += STEP) {
+            const bool whole = t0 + 32 * NS <= s.ctx && t0 + 32 * NS <= t_end && [&] {
+                bool all = true;
 #pragma unroll
-                            for (int e = 0; e < NV; ++e) {
-                                const int d = (4 * j + i) * NV + e;
-                                uint32_t bits;
-                                if constexpr (FP8) {
-                                    bits = H::from8(*reinterpret_cast<const uint8_t*>(row + d), false) & 0xffffu;
-                                } else {
-                                    bits = *reinterpret_cast<const uint16_t*>(row + 2 * d);
-                                }
-                                const float v = (float)__builtin_bit_cast(TQ, (uint16_t)bits);
-                                const bool nf = (bits & H::kExp) == H::kExp;
+                for (int k = 0; k < 2 * NS; ++k) all &= own(pa, k) >= 0;
+                return all;
+            }();
+            if constexpr (R > 1) {
+                // The row waves share their steps and go through the same number of them: when all have met, this
+                // step has arrived and the one before it is read, so its place takes the next one.
+                wait_loads<0>();
+                wait_and_meet();
+                const uint32_t next = at == tile0 ? at + NS * L::kBytes : tile0;
+                fetch(t0 + STEP, pb, next, 0, NC);
+                bool none = false;
 #pragma unroll
-                                for (int m = 0; m < MT; ++m) o[m][e][i] = nf && see[m] ? fmaf(pk[m], v, o[m][e][i]) : o[m][e][i];
-                            }
-                    }
+                for (int i = 0; i < NP; ++i) none |= pa.p[i] < 0;
+                if (tb + STEP > s.ctx || tb + STEP > t_end || none) {  // alike in all waves
+                    if (!whole) clean(at);  // each wave a share of its tiles, before any of them is read
+                    wait_and_meet();
+                }
+                if (t0 < t_end) step(at, whole);
+                at = next;
+            } else {
+                wait_loads<(NB > 1 ? NC : NC / 2)>();  // of two tiles under way the older one (one tile: its keys)
+                step(at, whole);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if constexpr (NB == 1) {
+                    fetch(t0 + STEP, pb, at, NC / 2, NC);
+                } else {
+                    fetch(t0 + 2 * STEP, pc, at, 0, NC);
+                    at = at == tile0 ? at + L::kBytes : tile0;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;  // high or low halves of two positions
-                u32x4 vt;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) vt[k] = __builtin_amdgcn_perm(w[2 * k + 1][e >> 1], w[2 * k][e >> 1], sel);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) o[m][e] = H::mfma(vt, pf[m], o[m][e]);
-            }
-            load_v(t0 + U, pn);
-            pg[0] = pn[0];
-            pg[1] = pn[1];
-            pn[0] = page_at(t0 + 2 * U);
-            pn[1] = page_at(t0 + 2 * U + 16);
+            t0 += STEP;
+            pa = pb;
+            pb = pc;
+            pc = pd;
+            pd = pages_at(tb + 4 * STEP);  // asked for steps before the transfers need it
         }
+        wait_loads<0>();  // what was fetched beyond the end
 
-        // join the position waves, then write: lane (c, j) has row c, dims 4 j NV .. + 4 NV of each tile
+        // Join the T waves of each row over positions: every one brings its rows to the common maximum, the
+        // first adds up. Lane (c, j) has row c, dims 16 e + 4 j .. + 3.
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             l[m] += __shfl_xor(l[m], 16);
             l[m] += __shfl_xor(l[m], 32);
         }
-        if constexpr (TW > 1) {
+        if constexpr (T > 1) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 if (j == 0) {
                     ml[tw][(rw * MT + m) * 16 + c][0] = mx[m];
                     ml[tw][(rw * MT + m) * 16 + c][1] = l[m];
                 }
-            __syncthreads();
+            __syncthreads();  // all tiles are read, all transfers done
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int r = (rw * MT + m) * 16 + c;
                 float top = kLow, sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < TW; ++w) top = fmaxf(top, ml[w][r][0]);
+                for (int w = 0; w < T; ++w) top = fmaxf(top, ml[w][r][0]);
 #pragma unroll
-                for (int w = 0; w < TW; ++w) sum += ml[w][r][1] * __builtin_amdgcn_exp2f(ml[w][r][0] - top);
+                for (int w = 0; w < T; ++w) sum += ml[w][r][1] * __builtin_amdgcn_exp2f(ml[w][r][0] - top);
                 const float f = __builtin_amdgcn_exp2f(mx[m] - top);
                 mx[m] = top;
                 l[m] = sum;
 #pragma unroll
-                for (int e = 0; e < NV; ++e) o[m][e] *= f;
-                if (tw > 0) {
-                    float* to = o_lds + ((tw - 1) * RB + r) * kRow + 4 * j * NV;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < NV; e += 4)
-                            *reinterpret_cast<f32x4*>(to + i * NV + e) = f32x4{o[m][e][i], o[m][e + 1][i], o[m][e + 2][i], o[m][e + 3][i]};
+                for (int e = 0; e < NE; ++e) {
+                    o[m][e] *= f;
+                    if (tw > 0) *reinterpret_cast<f32x4*>(o_lds + ((tw - 1) * RB + r) * kRow + 16 * e + 4 * j) = o[m][e];
                 }
             }
             __syncthreads();
@@ -551,150 +665,168 @@ __global__ __launch_bounds__(256) void k_attn(AttnArgs a) {
             for (int m = 0; m < MT; ++m) {
                 const int rl = (rw * MT + m) * 16 + c, r = blk * RB + rl;
                 if (r >= rows) continue;
-                if constexpr (TW > 1) {
 #pragma unroll
-                    for (int w = 0; w < TW - 1; ++w) {
-                        const float* from = o_lds + (w * RB + rl) * kRow + 4 * j * NV;
+                for (int w = 0; w < T - 1; ++w)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                    for (int e = 0; e < NE; ++e) o[m][e] += *reinterpret_cast<const f32x4*>(o_lds + (w * RB + rl) * kRow + 16 * e + 4 * j);
+                const int t = r / a.group, hq = h * a.group + (r - t * a.group);
+                if (odd[turn]) {  // what clean() took out: infinite or NaN for the rows that see it
+                    const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
+                    for (int x = max(s.ctx, u0 * U); x < t_end; ++x) {
+                        const int page = page_at(x);
+                        if (page < 0 || !((mask >> (x - s.ctx)) & 1)) continue;
+                        const char* v = vb + page * a.c.v_page + (int64_t)(x & pmask) * a.c.v_row + 4 * j * L::kElem;
 #pragma unroll
-                            for (int e = 0; e < NV; e += 4) {
-                                const f32x4 y = *reinterpret_cast<const f32x4*>(from + i * NV + e);
-                                o[m][e][i] += y.x;
-                                o[m][e + 1][i] += y.y;
-                                o[m][e + 2][i] += y.z;
-                                o[m][e + 3][i] += y.w;
+                        for (int e = 0; e < NE; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w;
+                                if constexpr (FP8)
+                                    w = H::from8(reinterpret_cast<const uint8_t*>(v)[16 * e + i], false) & 0xffffu;
+                                else
+                                    w = reinterpret_cast<const uint16_t*>(v)[16 * e + i];
+                                o[m][e][i] += (w & H::kExp) == H::kExp ? (float)__builtin_bit_cast(TQ, (uint16_t)w) : 0.f;
                             }
                     }
                 }
                 if (p.splits > 1) {
                     float* to = piece_rows(a, item, RB, D);
-                    float* row = to + rl * D + 4 * j * NV;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < NV; e += 4)
-                            *reinterpret_cast<f32x4*>(row + i * NV + e) = f32x4{o[m][e][i], o[m][e + 1][i], o[m][e + 2][i], o[m][e + 3][i]};
+                    for (int e = 0; e < NE; ++e) *reinterpret_cast<f32x4*>(to + rl * D + 16 * e + 4 * j) = o[m][e];
                     if (j == 0) {
                         to[RB * D + 2 * rl] = mx[m];
                         to[RB * D + 2 * rl + 1] = l[m];
                     }
                     continue;
                 }
-                const int t = r / a.group, hq = h * a.group + (r - t * a.group);
-                const float inv = l[m] > 0.f || l[m] != l[m] ? vs_scale / l[m] : 0.f;
-                TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + 4 * j * NV;
+                const bool any = l[m] > 0.f || l[m] != l[m];
+                const float inv = any ? vs_scale / l[m] : 0.f;
+                TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + 4 * j;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t y[NV / 2];
-#pragma unroll
-                    for (int e = 0; e < NV; e += 2) y[e / 2] = pack<TQ>(o[m][e][i] * inv, o[m][e + 1][i] * inv);
-#pragma unroll
-                    for (int e = 0; e < NV / 2; e += 2)
-                        *reinterpret_cast<u32x2*>(out + i * NV + 2 * e) = u32x2{y[e], y[e + 1]};
-                }
+                for (int e = 0; e < NE; ++e)
+                    *reinterpret_cast<u32x2*>(out + 16 * e) = u32x2{pack<TQ>(o[m][e][0] * inv, o[m][e][1] * inv),
+                                                                    pack<TQ>(o[m][e][2] * inv, o[m][e][3] * inv)};
                 if (a.lse && j == 0)
-                    a.lse[(int64_t)(s.q0 + t) * a.heads + hq] =
-                        l[m] > 0.f || l[m] != l[m] ? (mx[m] + __builtin_amdgcn_logf(l[m])) * kLn2 : -INFINITY;
+                    a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (mx[m] + __builtin_amdgcn_logf(l[m])) * kLn2 : -INFINITY;
             }
         }
-        if constexpr (TW > 1) __syncthreads();  // ml and o_lds are written again by the next piece
+        __syncthreads();  // the tiles, ml and o_lds are written again by the next piece
+        turn ^= 1;
     }
 }
 
-// Joins the pieces of the sequences that were split: a workgroup per (token, query head), its waves
-// taking every fourth piece, in an order that does not depend on timing.
-template <typename TQ, int D>
-__global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb, int unit) {
+// Joins the pieces of the sequences that were split: WAVES waves per (token, query head) of a sequence
+// and key/value head, in an order that does not depend on timing. Lane s of a wave takes the maximum
+// and sum of piece s, so that all pieces' rows are requested at once.
+template <typename TQ, int D, int WAVES>
+__global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     constexpr int N = D / 64;
     __shared__ float part[4][D + 2];
-    const int t = blockIdx.x, hq = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int lo = 0, hi = a.batch;  // the last b with q_start[b] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= t) lo = mid; else hi = mid;
-    }
-    const int b = lo;
-    const Seq s = seq_of(a, b);
-    const int i = t - s.q0;
-    if (i < 0 || i >= s.n) return;
+    const int b = blockIdx.x / a.c.heads, h = blockIdx.x - b * a.c.heads;
+    const int r = WAVES == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave;
     const int* head = reinterpret_cast<const int*>(a.ws + a.max_items * rb * (D + 2));
-    const int units = max(1, (int)(((int64_t)positions(a, s) + unit - 1) / unit));
-    const int splits = attn_splits(units, head[0]), blocks = (s.n * a.group + rb - 1) / rb;
-    if (splits <= 1) return;
-    const int h = hq / a.group, r = i * a.group + hq - h * a.group;
+    const int chunk = head[0], before = head[1 + b];
+    const Seq s = seq_of(a, b);
+    const Plan p = plan_of(a, s, rb, chunk);
+    if (p.splits <= 1 || r >= s.n * a.group) return;
     const int blk = r / rb, rl = r - blk * rb;
-    const int first = head[1 + b] + h * splits * blocks + blk;
+    const int first = before + h * p.splits * p.blocks + blk;
+    const int s0 = WAVES == 4 ? wave : 0;
     float m = kLow, l = 0.f, o[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int k = wave; k < splits; k += 4) {
-        const float* p = piece_rows(a, first + k * blocks, rb, D);
-        const float mk = p[rb * D + 2 * rl], lk = p[rb * D + 2 * rl + 1];
-        float y[N];
+    for (int k0 = s0; k0 < p.splits; k0 += 64 * WAVES) {
+        const int mine = k0 + lane * WAVES, count = min(64, (p.splits - k0 + WAVES - 1) / WAVES);
+        float mk = kLow, lk = 0.f;
+        if (lane < count) {
+            const float2 y = *reinterpret_cast<const float2*>(piece_rows(a, first + mine * p.blocks, rb, D) + rb * D + 2 * rl);
+            mk = y.x;
+            lk = y.y;
+        }
+        float to = mk;
 #pragma unroll
-        for (int e = 0; e < N; ++e) y[e] = p[rl * D + lane * N + e];
-        const float to = fmaxf(m, mk), f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(mk - to);
+        for (int d = 32; d; d >>= 1) to = fmaxf(to, __shfl_xor(to, d));
+        to = fmaxf(to, m);
+        const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(mk - to);
+        lk *= g;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) lk += __shfl_xor(lk, d);
         m = to;
-        l = l * f + lk * g;
+        l = l * f + lk;
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = o[e] * f + y[e] * g;
+        for (int e = 0; e < N; ++e) o[e] *= f;
+        for (int k = 0; k < count; ++k) {
+            const float* y = piece_rows(a, first + (k0 + k * WAVES) * p.blocks, rb, D) + rl * D + lane * N;
+            const float w = __shfl(g, k);
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = fmaf(y[e], w, o[e]);
+        }
     }
+    if constexpr (WAVES == 4) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) part[wave][lane * N + e] = o[e];
-    if (lane == 0) {
-        part[wave][D] = m;
-        part[wave][D + 1] = l;
+        for (int e = 0; e < N; ++e) part[wave][lane * N + e] = o[e];
+        if (lane == 0) {
+            part[wave][D] = m;
+            part[wave][D + 1] = l;
+        }
+        __syncthreads();
+        if (wave != 0) return;
+        float top = kLow;
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
+        l = 0.f;
+        m = top;
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = 0.f;
+        for (int w = 0; w < 4; ++w) {
+            const float f = __builtin_amdgcn_exp2f(part[w][D] - top);
+            l += part[w][D + 1] * f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = fmaf(part[w][lane * N + e], f, o[e]);
+        }
     }
-    __syncthreads();
-    if (wave != 0) return;
-    float top = kLow;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = 0.f;
-    for (int w = 0; w < 4; ++w) {
-        const float f = __builtin_amdgcn_exp2f(part[w][D] - top);
-        sum += part[w][D + 1] * f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] += part[w][lane * N + e] * f;
-    }
-    const bool any = sum > 0.f || sum != sum;
-    const float inv = any ? (a.c.v_scale ? a.c.v_scale[h] : 1.f) / sum : 0.f;
-    TQ* out = static_cast<TQ*>(a.out) + (int64_t)t * a.ldo + (int64_t)hq * D + lane * N;
+    const int t = r / a.group, hq = h * a.group + (r - t * a.group);
+    const bool any = l > 0.f || l != l;
+    const float inv = any ? (a.c.v_scale ? a.c.v_scale[h] : 1.f) / l : 0.f;
+    TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + lane * N;
 #pragma unroll
     for (int e = 0; e < N; ++e) out[e] = (TQ)(o[e] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)t * a.heads + hq] = any ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+    if (a.lse && lane == 0) a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-template <typename TQ, bool FP8, int D, int MT, int RW>
+template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-    constexpr int TW = 4 / RW, RB = 16 * MT * RW;
-    const size_t lds = (size_t)(TW - 1) * RB * (D + 4) * 4 + (a.target > 0 ? ((size_t)a.batch + 1) * 4 : 0);
-    int64_t wgs = a.target > 0 ? a.max_items
-                               : (int64_t)a.batch * a.c.heads * ((a.max_tree * a.group + RB - 1) / RB);
-    if (wgs > 2048) wgs = 2048;
-    k_attn<TQ, FP8, D, MT, RW><<<(unsigned)wgs, 256, lds, s>>>(a);
-    if (a.target > 0) k_join<TQ, D><<<dim3(a.tokens, a.heads), 256, 0, s>>>(a, RB, 32 * TW);
+    using C = Cfg<FP8, D, MT, R, T, NS, NB>;
+    const int64_t rows = (int64_t)a.max_tree * a.group, pairs = (int64_t)a.batch * a.c.heads;
+    const int64_t most = a.target > 0 ? a.max_items : pairs * cdiv(rows, C::RB);
+    const int64_t wgs = most < kCus * C::kPerCu ? cdiv(most, 8) * 8 : kCus * C::kPerCu;
+    const unsigned lds = a.target > 0 ? (unsigned)(a.batch + 1) * 4 : 0;
+    k_attn<TQ, FP8, D, MT, R, T, NS, NB><<<(unsigned)wgs, C::kThreads, lds, s>>>(a);
+    if (a.target > 0) {
+        // few rows: many pieces each, four waves share them
+        if (rows * pairs <= 1024)
+            k_join<TQ, D, 4><<<dim3((unsigned)pairs, (unsigned)rows), 256, 0, s>>>(a, C::RB);
+        else
+            k_join<TQ, D, 1><<<dim3((unsigned)pairs, (unsigned)cdiv(rows, 4)), 256, 0, s>>>(a, C::RB);
+    }
     return hipGetLastError();
 }
 template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const AttnArgs& a, AttnTile t, hipStream_t s) {
     if constexpr (D == 256) {
-        return t.row_waves == 1 ? launch<TQ, FP8, D, 1, 1>(a, s) : t.row_waves == 2 ? launch<TQ, FP8, D, 1, 2>(a, s)
-                                                                                    : launch<TQ, FP8, D, 1, 4>(a, s);
+        return t.row_waves == 1 ? launch<TQ, FP8, D, 1, 1, 2, 1, 2>(a, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2>(a, s);
     } else {
-        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1>(a, s);
-        return t.row_waves == 1 ? launch<TQ, FP8, D, 2, 1>(a, s) : t.row_waves == 2 ? launch<TQ, FP8, D, 2, 2>(a, s)
-                                                                                    : launch<TQ, FP8, D, 2, 4>(a, s);
+        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1, 4, 1, (FP8 || D == 64) ? 2 : 1>(a, s);
+        return t.row_waves == 1   ? launch<TQ, FP8, D, 2, 1, 4, 1, (FP8 || D == 64) ? 2 : 1>(a, s)
+               : t.row_waves == 2 ? launch<TQ, FP8, D, 2, 2, 2, 1, 2>(a, s)
+                                  : launch<TQ, FP8, D, 2, 4, 1, 2, 2>(a, s);
     }
 }
 template <typename TQ, bool FP8>
 hipError_t launch_d(const AttnArgs& a, int d, AttnTile t, hipStream_t s) {
-    return d == 64 ? launch_t<TQ, FP8, 64>(a, t, s) : d == 128 ? launch_t<TQ, FP8, 128>(a, t, s) : launch_t<TQ, FP8, 256>(a, t, s);
+    return d == 64    ? launch_t<TQ, FP8, 64>(a, t, s)
+           : d == 128 ? launch_t<TQ, FP8, 128>(a, t, s)
+                      : launch_t<TQ, FP8, 256>(a, t, s);
 }
 
 }  // namespace

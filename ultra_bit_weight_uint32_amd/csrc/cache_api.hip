@@ -83,7 +83,8 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
 int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_heads, int head_dim, size_t* out) {
     if (!out || batch < 0 || max_tree < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0) return UBW_EINVAL;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return UBW_EUNSUPPORTED;
-    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || heads > 65536 || kv_heads > 4096) return UBW_ERANGE;
+    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || heads > 65536 || kv_heads > 4096 || heads / kv_heads > 1024)
+        return UBW_ERANGE;
     const int64_t rows = (int64_t)max_tree * (heads / kv_heads);
     *out = (size_t)attn_workspace_floats(batch, rows, kv_heads, head_dim, attn_tile(rows, head_dim)) * 4;
     return UBW_OK;
@@ -100,7 +101,8 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     if (st != UBW_OK) return st;
     if (heads % c.kv_heads != 0) return UBW_EINVAL;
     if (!half_type(q_dtype) || (c.dtype != UBW_E4M3 && c.dtype != q_dtype)) return UBW_EUNSUPPORTED;
-    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536) return UBW_ERANGE;
+    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536 || heads / c.kv_heads > 1024)
+        return UBW_ERANGE;
     if (tokens == 0 || batch == 0) return UBW_OK;
     if (!q_start || !ctx_len) return UBW_EINVAL;
     if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
@@ -116,7 +118,7 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     if (workspace && ws_bytes < need) return UBW_ESIZE;
     const int64_t rows = (int64_t)max_tree * (heads / c.kv_heads);
     const AttnTile t = attn_tile(rows, c.head_dim);
-    if (attn_max_items(batch, rows, c.kv_heads, t) > kMaxGrid) return UBW_ERANGE;
+    if (attn_max_items(batch, rows, c.kv_heads, c.head_dim, t) > kMaxGrid) return UBW_ERANGE;
     AttnArgs a{};
     a.c = pages_of(c);
     a.q = q;
@@ -137,10 +139,10 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     a.scale = scale;
     a.lse = lse;
     a.ws = static_cast<float*>(workspace);
-    a.max_items = attn_max_items(batch, rows, c.kv_heads, t);
+    a.max_items = attn_max_items(batch, rows, c.kv_heads, c.head_dim, t);
     // contexts of one unit (or known to be) are not split: one launch
     const int64_t longest = max_len > 0 ? max_len : (int64_t)table_cols * c.page_size;
-    a.target = workspace && longest > attn_unit(t) ? kAttnItems : 0;
+    a.target = workspace && longest > kAttnUnit ? attn_target(t, c.head_dim) : 0;
     return hip_status(launch_attn(a, c.dtype, q_dtype, c.head_dim, t, as_stream(stream)));
 }
 

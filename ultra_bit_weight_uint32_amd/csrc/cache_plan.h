@@ -82,20 +82,16 @@ inline int check_pool(const ubw_page_pool* p) {
 
 // ---- tree attention -------------------------------------------------------------------------
 // The rows of a (sequence, key/value head): row r is token r / G, query head h G + r % G (G =
-// heads / kv_heads). A workgroup takes a block of rows and a run of positions; its four waves are
-// row_waves groups of 16 tiles rows each, the others splitting the positions in units of 32.
+// heads / kv_heads). A workgroup takes a block of rows and a run of positions, in units of 128.
+// row_waves waves lie side by side over rows, each with `tiles` times 16 of them; waves over the same
+// rows (four or two with one row wave, two with two) take 32 positions in turn.
 struct AttnTile {
-    int tiles;      // 16-row tiles a wave keeps (they share the loaded keys and values)
-    int row_waves;  // waves side by side over rows: 1, 2 or 4 (4 / row_waves over positions)
+    int tiles, row_waves;
 };
-constexpr int kAttnItems = 1024;  // aimed-at number of pieces when contexts are split
+constexpr int kAttnUnit = 128;
 UBW_HD inline int attn_rows(AttnTile t) { return 16 * t.tiles * t.row_waves; }
-UBW_HD inline int attn_unit(AttnTile t) { return 32 * (4 / t.row_waves); }  // positions per step of the workgroup
-
 inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
-    if (head_dim == 256) {  // the sums of 256 dims take 64 registers per tile: one tile a wave
-        return AttnTile{1, max_rows <= 16 ? 1 : max_rows <= 32 ? 2 : 4};
-    }
+    if (head_dim == 256) return AttnTile{1, max_rows <= 16 ? 1 : 4};  // the sums of 256 dims take 64 registers per tile
     if (max_rows <= 16) return AttnTile{1, 1};
     if (max_rows <= 32) return AttnTile{2, 1};
     if (max_rows <= 64) return AttnTile{2, 2};
@@ -104,10 +100,17 @@ inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
 
 // How a batch is cut: sequence b has blocks_b row blocks of units_b units of positions for each
 // key/value head; a piece is one block over `chunk` units at most, a sequence's pieces of equal size
-// but for one unit. chunk is the smallest for which about kAttnItems pieces arise.
+// but for one unit. chunk starts at total / target and grows while there are more pieces than that.
+// How many pieces a batch is aimed to have: about three for each workgroup that is resident with one row
+// wave, one with more (their sums are larger).
+inline int attn_target(AttnTile t, int head_dim) { return t.row_waves == 1 ? 1536 : head_dim == 64 ? 768 : 512; }
 UBW_HD inline int attn_chunk(int64_t total_units, int target) {
     const int64_t c = (total_units + target - 1) / target;
     return (int)(c < 1 ? 1 : c);
+}
+UBW_HD inline int attn_larger_chunk(int chunk, int64_t pieces, int target) {
+    const int64_t c = (chunk * pieces + target - 1) / target;
+    return (int)(c > chunk ? c : chunk + 1);
 }
 UBW_HD inline int attn_splits(int units, int chunk) { return units == 0 ? 0 : (units + chunk - 1) / chunk; }
 UBW_HD inline void attn_range(int units, int splits, int s, int* u0, int* u1) {
@@ -116,14 +119,14 @@ UBW_HD inline void attn_range(int units, int splits, int s, int* u0, int* u1) {
     *u1 = *u0 + q + (s < r ? 1 : 0);
 }
 // Most pieces of a batch: the sum over sequences of blocks kv ceil(units / chunk) is at most
-// total / chunk + batch blocks kv <= kAttnItems + batch blocks kv.
-inline int64_t attn_max_items(int batch, int64_t max_rows, int kv_heads, AttnTile t) {
-    return kAttnItems + (int64_t)batch * cdiv(max_rows, attn_rows(t)) * kv_heads;
+// total / chunk + batch blocks kv <= target + batch blocks kv.
+inline int64_t attn_max_items(int batch, int64_t max_rows, int kv_heads, int head_dim, AttnTile t) {
+    return attn_target(t, head_dim) + (int64_t)batch * cdiv(max_rows, attn_rows(t)) * kv_heads;
 }
 // Scratch floats: each piece's rows (head_dim sums, then the running maximum and the sum of weights),
 // then the cut itself (units per piece, each sequence's first piece).
 inline int64_t attn_workspace_floats(int batch, int64_t max_rows, int kv_heads, int head_dim, AttnTile t) {
-    return attn_max_items(batch, max_rows, kv_heads, t) * attn_rows(t) * (head_dim + 2) + batch + 1;
+    return attn_max_items(batch, max_rows, kv_heads, head_dim, t) * attn_rows(t) * (head_dim + 2) + batch + 1;
 }
 
 }  // namespace cache
