@@ -14,67 +14,79 @@ KVCache and PagePool hold the tensors and their descriptors, checked once; the c
 changes from call to call. Every call runs on its tensors' device, on that device's current stream.
 """
 import ctypes
-import math
 
 import torch
 
-from . import (UBW_BF16, UBW_E4M3, UBW_F16, UBW_F32, KVCacheDesc, PagePoolDesc, _check, lib)
+from . import UBW_BF16, UBW_E4M3, UBW_F16, UBW_F32, KVCacheDesc, PagePoolDesc, _check, lib
 
 _TYPES = {torch.float32: UBW_F32, torch.float16: UBW_F16, torch.bfloat16: UBW_BF16, torch.float8_e4m3fn: UBW_E4M3}
 
 
-class _On:
-    """The device of a call: its stream, made current for the launch where it is not."""
-    __slots__ = ("device", "before")
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _flat(t, name, dtype, device, numel=None, shape=None, at_least=False):
-    """Pointer of a contiguous tensor of a dtype on the call's device."""
+def _launch(fn, index, *args):
+    """The call of a library function on a device, on that device's current stream."""
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == index:
+        st = f(*args, _current_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, _current_stream(index))
+    if st:
+        _check(fn, st)
+
+
+def _elsewhere(t, name, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{index}")
+
+
+def _flat(t, name, dtype, index, numel=None, shape=None):
+    """Pointer of a contiguous tensor of a dtype on the call's device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, name, index)
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if numel is not None and (t.numel() < numel if at_least else t.numel() != numel):
+    if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
     return t.data_ptr()
 
 
-def _rows(t, name, device, dim, heads=None, tokens=None, dtype=None):
-    """(pointer, row stride) of [tokens, heads, dim] whose heads are contiguous; rows may be apart (a
-    part of a fused buffer)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or \
-            (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name} must be [{tokens if tokens is not None else 'tokens'}, "
-                         f"{heads if heads is not None else 'heads'}, {dim}], got {list(t.shape)}")
+def _rows(t, name, index, dim, heads=None, tokens=None, dtype=None):
+    """(pointer, row stride, tokens, heads) of [tokens, heads, dim] whose heads are contiguous; rows may
+    be apart (a part of a fused buffer)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, name, index)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {list(t.shape)}")
+    n, h, d = t.shape
+    if d != dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
+        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, {dim}], got {list(t.shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    st = t.stride()
-    if st[2] != 1 or (t.shape[1] > 1 and st[1] != dim):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != dim):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else t.shape[1] * dim
+    return t.data_ptr(), s0 if n > 1 else h * dim, n, h
+
+
+def _table(t, batch, index):
+    """(pointer, row stride, columns) of an int32 [batch, columns] table; rows may be apart."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, "table", index)
+    if t.dim() != 2 or t.shape[0] != batch or t.dtype is not torch.int32 or t.shape[1] < 1 or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"table must be int32 [{batch}, columns] with contiguous columns")
+    cols = t.shape[1]
+    return t.data_ptr(), t.stride(0) if batch > 1 else cols, cols
 
 
 class KVCache:
@@ -96,7 +108,7 @@ class KVCache:
         if k.dtype is not torch.float8_e4m3fn and (k_scale is not None or v_scale is not None):
             raise ValueError("scales belong to 8-bit caches")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.index, self.dtype = k.device, k.get_device(), k.dtype
         k5, v5 = (x if x.dim() == 5 else x[None] for x in (k, v))
         self.layers, self.pages, self.kv_heads, self.page_size, self.head_dim = k5.shape
         d = KVCacheDesc()
@@ -106,7 +118,7 @@ class KVCache:
         d.k_stride[:], d.v_stride[:] = k5.stride()[:4], v5.stride()[:4]
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is not None:
-                setattr(d, name, _flat(s, name, torch.float32, self.device, numel=self.kv_heads))
+                setattr(d, name, _flat(s, name, torch.float32, self.index, self.kv_heads))
         self.desc, self.ref = d, ctypes.byref(d)
 
     def layer(self, i):
@@ -123,30 +135,27 @@ def qk_norm_rope(q, k, v, cache, positions, slots, inv_freq, q_weight=None, k_we
     at slots (int32 [tokens]; outside the cache: not stored) of the cache. q [tokens, heads, head_dim],
     k, v [tokens, kv_heads, head_dim] in fp32, fp16 or bf16. Returns the queries [tokens, heads,
     head_dim] in out (or a new tensor of out_dtype; default the cache's type, fp16 for 8 bits)."""
-    dev, dim, kvh = cache.device, cache.head_dim, cache.kv_heads
-    qp, ldq = _rows(q, "q", dev, dim)
-    t, heads = q.shape[0], q.shape[1]
-    kp, ldk = _rows(k, "k", dev, dim, kvh, t, q.dtype)
-    vp, ldv = _rows(v, "v", dev, dim, kvh, t, q.dtype)
-    if q.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise TypeError(f"q has dtype {q.dtype}, expected float32, float16 or bfloat16")
+    dev, dim, kvh = cache.index, cache.head_dim, cache.kv_heads
+    dtype = q.dtype
+    qp, ldq, t, heads = _rows(q, "q", dev, dim)
+    kp, ldk, _, _ = _rows(k, "k", dev, dim, kvh, t, dtype)
+    vp, ldv, _, _ = _rows(v, "v", dev, dim, kvh, t, dtype)
+    if dtype is torch.float8_e4m3fn or dtype not in _TYPES:
+        raise TypeError(f"q has dtype {dtype}, expected float32, float16 or bfloat16")
     if out is None:
         if out_dtype is None:
             out_dtype = torch.float16 if cache.dtype is torch.float8_e4m3fn else cache.dtype
-        out = torch.empty((t, heads, dim), dtype=out_dtype, device=dev)
-    if out.dtype not in (torch.float16, torch.bfloat16):
+        out = torch.empty((t, heads, dim), dtype=out_dtype, device=cache.device)
+    op, ldo, _, _ = _rows(out, "out", dev, dim, heads, t)
+    if out.dtype is not torch.float16 and out.dtype is not torch.bfloat16:
         raise TypeError(f"out has dtype {out.dtype}, expected float16 or bfloat16")
-    op, ldo = _rows(out, "out", dev, dim, heads, t)
     f32, i32 = torch.float32, torch.int32
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    with _On(dev) as stream:
-        _check("ubw_qk_norm_rope", lib().ubw_qk_norm_rope(
-            cache.ref, qp, ldq, kp, ldk, vp, ldv, _TYPES[q.dtype], t, heads,
+    _launch("ubw_qk_norm_rope", dev, cache.ref, qp, ldq, kp, ldk, vp, ldv, _TYPES[dtype], t, heads,
             None if q_weight is None else _flat(q_weight, "q_weight", f32, dev, dim),
             None if k_weight is None else _flat(k_weight, "k_weight", f32, dev, dim), eps,
             None if rot == 0 else _flat(inv_freq, "inv_freq", f32, dev), rot, 1 if interleaved else 0,
-            _flat(positions, "positions", i32, dev, t), _flat(slots, "slots", i32, dev, t), op, _TYPES[out.dtype], ldo,
-            stream))
+            _flat(positions, "positions", i32, dev, t), _flat(slots, "slots", i32, dev, t), op, _TYPES[out.dtype], ldo)
     return out
 
 
@@ -167,59 +176,51 @@ def tree_attn(q, cache, table, q_start, ctx_len, masks=None, *, max_tree, max_le
     sequence has; max_len: the longest context plus tokens (0: unknown). lse: None or fp32 [tokens,
     heads] to be written. workspace: tree_attn_workspace() (None: long contexts are not split over
     workgroups). Returns out [tokens, heads, head_dim] in q's type."""
-    dev, dim = cache.device, cache.head_dim
-    qp, ldq = _rows(q, "q", dev, dim)
-    t, heads = q.shape[0], q.shape[1]
-    if q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q has dtype {q.dtype}, expected float16 or bfloat16")
+    dev, dim = cache.index, cache.head_dim
+    qp, ldq, t, heads = _rows(q, "q", dev, dim)
+    dtype = q.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"q has dtype {dtype}, expected float16 or bfloat16")
     if out is None:
-        out = torch.empty((t, heads, dim), dtype=q.dtype, device=dev)
-    op, ldo = _rows(out, "out", dev, dim, heads, t, q.dtype)
+        out = torch.empty((t, heads, dim), dtype=dtype, device=cache.device)
+    op, ldo, _, _ = _rows(out, "out", dev, dim, heads, t, dtype)
     i32 = torch.int32
     batch = ctx_len.numel()
-    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not i32 or table.device != dev or \
-            table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be int32 [{batch}, columns] with contiguous columns on {dev}")
-    if masks is not None and masks.dtype not in (torch.int64, torch.uint64):
-        raise TypeError(f"masks has dtype {masks.dtype}, expected int64 or uint64")
+    tp, ld_table, cols = _table(table, batch, dev)
+    if masks is not None:
+        if masks.dtype is not torch.int64 and masks.dtype is not torch.uint64:
+            raise TypeError(f"masks has dtype {masks.dtype}, expected int64 or uint64")
+        masks = _flat(masks, "masks", masks.dtype, dev, t)
     ws, wsb = None, 0
     if workspace is not None:
-        ws, wsb = _flat(workspace, "workspace", workspace.dtype, dev), workspace.numel() * workspace.element_size()
-    with _On(dev) as stream:
-        _check("ubw_tree_attn", lib().ubw_tree_attn(
-            cache.ref, qp, _TYPES[q.dtype], ldq, t, heads, _flat(q_start, "q_start", i32, dev, batch + 1),
-            _flat(ctx_len, "ctx_len", i32, dev), batch, table.data_ptr(),
-            table.stride(0) if batch > 1 else table.shape[1], table.shape[1], max_tree, max_len,
-            None if masks is None else _flat(masks, "masks", masks.dtype, dev, t),
-            1 / math.sqrt(dim) if scale is None else scale, op, ldo,
-            None if lse is None else _flat(lse, "lse", torch.float32, dev, shape=(t, heads)), ws, wsb, stream))
+        ws, wsb = _flat(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
+    _launch("ubw_tree_attn", dev, cache.ref, qp, _TYPES[dtype], ldq, t, heads,
+            _flat(q_start, "q_start", i32, dev, batch + 1), _flat(ctx_len, "ctx_len", i32, dev), batch, tp, ld_table, cols,
+            max_tree, max_len, masks, dim ** -0.5 if scale is None else scale, op, ldo,
+            None if lse is None else _flat(lse, "lse", torch.float32, dev, shape=(t, heads)), ws, wsb)
     return out
 
 
 def cache_copy_pages(cache, pairs):
     """Page pairs[i, 0] copied to page pairs[i, 1] (int32 [count, 2]), keys and values of every layer.
     Pairs with an entry outside the cache's pages, as (-1, -1), are skipped."""
+    p = _flat(pairs, "pairs", torch.int32, cache.index)
     if pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError(f"pairs must be [count, 2], got {list(pairs.shape)}")
-    with _On(cache.device) as stream:
-        _check("ubw_cache_copy_pages", lib().ubw_cache_copy_pages(
-            cache.ref, _flat(pairs, "pairs", torch.int32, cache.device), pairs.shape[0], stream))
+    _launch("ubw_cache_copy_pages", cache.index, cache.ref, p, pairs.shape[0])
 
 
 def cache_compact(cache, table, ctx_len, keep):
     """Keys and values at position ctx_len[b] + keep[b, i] moved to ctx_len[b] + i in every layer, for
     i = 0, 1, ... up to the first entry of keep (int32 [batch, width]) that does not ascend from 0."""
-    dev, i32 = cache.device, torch.int32
+    dev, i32 = cache.index, torch.int32
+    kp = _flat(keep, "keep", i32, dev)
     if keep.dim() != 2:
         raise ValueError(f"keep must be [batch, width], got {list(keep.shape)}")
     batch, width = keep.shape
-    if table.dim() != 2 or table.shape[0] != batch or table.dtype is not i32 or table.device != dev or \
-            table.shape[1] < 1 or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be int32 [{batch}, columns] with contiguous columns on {dev}")
-    with _On(dev) as stream:
-        _check("ubw_cache_compact", lib().ubw_cache_compact(
-            cache.ref, table.data_ptr(), table.stride(0) if batch > 1 else table.shape[1], table.shape[1],
-            _flat(ctx_len, "ctx_len", i32, dev, batch), _flat(keep, "keep", i32, dev), width, batch, stream))
+    tp, ld_table, cols = _table(table, batch, dev)
+    _launch("ubw_cache_compact", dev, cache.ref, tp, ld_table, cols, _flat(ctx_len, "ctx_len", i32, dev, batch), kp,
+            width, batch)
 
 
 class PagePool:
@@ -233,9 +234,9 @@ class PagePool:
         if not ref.is_cuda:
             raise ValueError("ref must be on a GPU (no CPU path exists)")
         self.ref, self.free, self.table, self.held, self.len, self.status = ref, free, table, held, len, status
-        self.device, self.page_size = ref.device, page_size
+        self.device, self.index, self.page_size = ref.device, ref.get_device(), page_size
         self.pages, (self.seqs, self.max_pages) = ref.numel(), table.shape
-        i32, dev = torch.int32, self.device
+        i32, dev = torch.int32, self.index
         d = PagePoolDesc()
         d.ref = _flat(ref, "ref", i32, dev)
         d.free_bits = _flat(free, "free", i32, dev, numel=-(-self.pages // 32))
@@ -254,33 +255,27 @@ def page_pool(pages, page_size, seqs, max_pages, device="cuda"):
     new = [torch.empty(n, dtype=torch.int32, device=device)
            for n in (pages, -(-pages // 32), (seqs, max_pages), seqs, seqs, 1)]
     pool = PagePool(*new, page_size)
-    with _On(pool.device) as stream:
-        _check("ubw_pages_init", lib().ubw_pages_init(pool.byref, stream))
+    _launch("ubw_pages_init", pool.index, pool.byref)
     return pool
 
 
 def pages_trim(pool, new_len):
     """len[s] = new_len[s] where that is not negative (int32 [seqs]), the pages behind it given back."""
-    p = _flat(new_len, "new_len", torch.int32, pool.device, pool.seqs)
-    with _On(pool.device) as stream:
-        _check("ubw_pages_trim", lib().ubw_pages_trim(pool.byref, p, stream))
+    _launch("ubw_pages_trim", pool.index, pool.byref, _flat(new_len, "new_len", torch.int32, pool.index, pool.seqs))
 
 
 def pages_fork(pool, parents):
     """Sequence s becomes a copy of parents[s] where that is not negative (int32 [seqs]), by sharing."""
-    p = _flat(parents, "parents", torch.int32, pool.device, pool.seqs)
-    with _On(pool.device) as stream:
-        _check("ubw_pages_fork", lib().ubw_pages_fork(pool.byref, p, stream))
+    _launch("ubw_pages_fork", pool.index, pool.byref, _flat(parents, "parents", torch.int32, pool.index, pool.seqs))
 
 
 def pages_reserve(pool, room, pairs=None):
     """Pages for room[s] more tokens of each sequence (int32 [seqs]). Returns pairs, int32 [seqs, 2]:
     (old, new) where a sequence got its own copy of a shared page, to be passed to cache_copy_pages
     before the pool's next call; (-1, -1) elsewhere."""
-    p = _flat(room, "room", torch.int32, pool.device, pool.seqs)
+    p = _flat(room, "room", torch.int32, pool.index, pool.seqs)
     if pairs is None:
         pairs = torch.empty((pool.seqs, 2), dtype=torch.int32, device=pool.device)
-    with _On(pool.device) as stream:
-        _check("ubw_pages_reserve", lib().ubw_pages_reserve(
-            pool.byref, p, _flat(pairs, "pairs", torch.int32, pool.device, shape=(pool.seqs, 2)), stream))
+    _launch("ubw_pages_reserve", pool.index, pool.byref, p,
+            _flat(pairs, "pairs", torch.int32, pool.index, shape=(pool.seqs, 2)))
     return pairs

@@ -108,6 +108,15 @@ __device__ inline Seq seq_of(const AttnArgs& a, int b) {
     s.ctx = max(a.ctx_len[b], 0);
     return s;
 }
+__device__ inline Seq seq_at(const AttnArgs& a, int b) {  // the same for a wave-uniform b
+    Seq s;
+    const ScalarWord* start = scalar_words(a.q_start) + b;
+    const int q0 = min(max((int)start[0], 0), a.tokens), q1 = min(max((int)start[1], q0), a.tokens);
+    s.q0 = q0;
+    s.n = min(q1 - q0, a.max_tree);
+    s.ctx = max((int)scalar_words(a.ctx_len)[b], 0);
+    return s;
+}
 // positions there are: the table ends them
 __device__ inline int positions(const AttnArgs& a, const Seq& s) {
     const int64_t most = (int64_t)a.table_cols << a.c.lps;
@@ -279,7 +288,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     using C = Cfg<FP8, D, MT, R, T, NS, NB>;
     constexpr int NE = D / 16, KS = D / 32, RB = C::RB, U = kAttnUnit, STEP = 32 * NS * T;
     constexpr int NC = (L::CK + L::CV) / R;  // transfers of a wave per tile
-    constexpr int NP = 2 * NS * (R > 1 ? T : 1);  // pages of a step that a wave knows
+    constexpr int NP = 2 * NS;  // pages of a wave's part of a step
     constexpr int kRow = D + 4;              // LDS row of o, in floats
     static_assert((L::CK + L::CV) % R == 0, "pieces of a tile are shared out evenly");
     static_assert(R > 1 ? NB == 2 : NS == 1, "shared steps are double-buffered, private ones have one tile");
@@ -339,7 +348,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 if (pre[mid] <= item) lo = mid; else hi = mid;
             }
             b = __builtin_amdgcn_readfirstlane(lo);
-            s = seq_of(a, b);
+            s = seq_at(a, b);
             p = plan_of(a, s, RB, chunk);
             int r = item - __builtin_amdgcn_readfirstlane(pre[b]);
             blk = r % p.blocks;
@@ -351,7 +360,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             const int r = item / blocks_max;
             h = r % a.c.heads;
             b = r / a.c.heads;
-            s = seq_of(a, b);
+            s = seq_at(a, b);
             p = plan_of(a, s, RB, 0);
             split = 0;
             if (blk >= p.blocks) continue;
@@ -371,22 +380,17 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             const int pg = table[t >> lps];
             return (uint32_t)pg < (uint32_t)a.c.pages ? pg : -1;
         };
-        // Pages of a step's positions, sixteen at a time: of this wave's tile, or with R > 1 of all tiles of the
-        // step (whether the waves meet to clean them is decided alike in all).
-        struct Pg {
+        struct Pg {  // pages of the positions of this wave's tiles, sixteen at a time
             int p[NP];
         };
-        const auto pages_at = [&](int t) {  // t: first position of the step, or of the tile
+        const auto pages_at = [&](int t) {
             Pg g;
 #pragma unroll
             for (int i = 0; i < NP; ++i) g.p[i] = page_at(t + 16 * i);
             return g;
         };
-        const auto own = [&](const Pg& g, int sub) {  // of sixteen positions of this wave's tiles
-            return R > 1 && T > 1 && tw == 1 ? g.p[(2 * NS) % NP + sub] : g.p[sub];
-        };
-        // The transfers of this wave for the step at t, those from first to last of each tile; rows that are not
-        // needed or on no page arrive as zeros.
+        // The transfers of this wave for the step at t, those from first to last of each tile; rows behind the
+        // end or on no page arrive as zeros.
         const auto fetch = [&](int t, const Pg& pg, uint32_t at, int first, int last) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -397,24 +401,30 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     if (i < first || i >= last) continue;
                     if (ch < L::CK) {
                         const int sub = ch / L::KL, piece = ch % L::KL;
-                        const int page = sub ? own(pg, 2 * n + 1) : own(pg, 2 * n);
-                        to_lds<0>(rows16(kb + (page < 0 ? 0 : page) * a.c.k_page + (int64_t)((t + 32 * n + 16 * sub) & pmask) * a.c.k_row + piece * 64,
-                                         page < 0 ? 0u : 16 * a.c.k_row - piece * 64), koff, to);
+                        const int page = sub ? pg.p[2 * n + 1] : pg.p[2 * n], x = t + 32 * n + 16 * sub;
+                        to_lds<0>(rows16(kb + (page < 0 ? 0 : page) * a.c.k_page + (int64_t)(x & pmask) * a.c.k_row + piece * 64,
+                                         page < 0 ? 0u : min(16, t_end - x) * a.c.k_row - piece * 64), koff, to);
                     } else {
                         const int row = (ch - L::CK) * L::RP, sub = row >> 4;  // of the tile
-                        const int page = sub ? own(pg, 2 * n + 1) : own(pg, 2 * n);
+                        const int page = sub ? pg.p[2 * n + 1] : pg.p[2 * n], x = t + 32 * n + row;
                         const uint32_t off = (uint32_t)vt * a.c.v_row + (uint32_t)((vp ^ L::mix((row + vt) & 15)) * 16);
-                        to_lds<0>(rows16(vb + (page < 0 ? 0 : page) * a.c.v_page + (int64_t)((t + 32 * n + row) & pmask) * a.c.v_row,
-                                         page < 0 ? 0u : L::RP * a.c.v_row), off, to);
+                        to_lds<0>(rows16(vb + (page < 0 ? 0 : page) * a.c.v_page + (int64_t)(x & pmask) * a.c.v_row,
+                                         page < 0 ? 0u : min(L::RP, max(t_end - x, 0)) * a.c.v_row), off, to);
                     }
                 }
         };
         int t0 = u0 * U + 32 * NS * tw;
         const int base = R > 1 ? u0 * U : t0;
-        Pg pa = pages_at(base), pb = pages_at(base + STEP), pc = pages_at(base + 2 * STEP), pd = pages_at(base + 3 * STEP);
+        Pg pa = pages_at(t0), pb = pages_at(t0 + STEP), pc = pages_at(t0 + 2 * STEP), pd = pages_at(t0 + 3 * STEP);
         fetch(t0, pa, tile0, 0, NC);
         if constexpr (R == 1 && NB == 2) fetch(t0 + STEP, pb, tile0 + L::kBytes, 0, NC);
 
+        uint64_t mask[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int t = min(r0 + 16 * m, rows - 1) / a.group;
+            mask[m] = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
+        }
         // queries: the B operand of S^T (8-bit keys come 16 dims a lane, so 32-dim steps take the dims
         // 64 s + 16 j + 8 half ..)
         u32x4 q[MT][KS];
@@ -436,12 +446,14 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         }
         const float cc = c2 * ks_scale;
 
-        // The compiler waits for the queries here, once, instead of at their first use in the loop, where it
+        // The compiler waits for queries and masks here, once, instead of at their first use in the loop, where it
         // would wait for all transfers under way as well.
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+            asm volatile("" : "+v"(mask[m]));
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) asm volatile("" : "+v"(q[m][ks]));
+        }
 
         f32x4 o[MT][NE];
         float mx[MT], l[MT];
@@ -491,37 +503,29 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         };
         // Hides from row tile m the positions of the step at t0 that it does not see.
         const auto hide = [&](int m, f32x4 (&sc)[2 * NS]) {
-            const int t = min(r0 + 16 * m, rows - 1) / a.group;
-            const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
 #pragma unroll
             for (int sub = 0; sub < 2 * NS; ++sub) {
                 const int x = t0 + 16 * sub + 4 * j;
-                const uint32_t there = own(pa, sub) < 0 ? 0u : (1u << min(max(t_end - x, 0), 4)) - 1;
-                const uint32_t sees = four_seen(mask, x - s.ctx) & there;
+                const uint32_t there = pa.p[sub] < 0 ? 0u : (1u << min(max(t_end - x, 0), 4)) - 1;
+                const uint32_t sees = four_seen(mask[m], x - s.ctx) & there;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sc[sub][k] = (sees >> k) & 1 ? sc[sub][k] : -INFINITY;
             }
         };
-        // Values that are no part of a sum must not reach it even as 0 * NaN: rows of the tile behind the
-        // sequence or on no page become zeros in LDS, and so do values of the tree that are not finite (set
-        // aside: `odd` asks for them at the end).
+        // Values of the tree that are not finite become zeros in LDS, so that they do not reach the rows that do
+        // not see them as 0 * NaN; `odd` asks for them at the end. (Rows behind the end or on no page are zeros.)
         const auto clean = [&](uint32_t at) {
             bool found = false;
-            for (int n = rw * 64 + lane; n < 32 * NS * L::P; n += 64 * R) {
-                const int row = n / L::P, x = t0 + row;
-                u32x4* w = lds_at<u32x4>(at + (row >> 5) * L::kBytes + L::CK * 1024 + (n % (32 * L::P)) * 16);
-                bool none = x >= t_end;
+            const int first = max(s.ctx - t0, 0), last = min(t_end - t0, 32 * NS);
+            for (int n = first * L::P + rw * 64 + lane; n < last * L::P; n += 64 * R) {
+                u32x4* w = lds_at<u32x4>(at + (n / (32 * L::P)) * L::kBytes + L::CK * 1024 + (n % (32 * L::P)) * 16);
+                u32x4 y = *w, nf;
 #pragma unroll
-                for (int k = 0; k < 2 * NS; ++k) none |= row >> 4 == k && own(pa, k) < 0;
-                const bool tree = x >= s.ctx;
-                u32x4 y = *w;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t nf = not_finite<TQ, FP8>(y[k]);
-                    found |= tree && !none && nf != 0;
-                    y[k] = none ? 0u : tree ? y[k] & ~nf : y[k];
+                for (int k = 0; k < 4; ++k) nf[k] = not_finite<TQ, FP8>(y[k]);
+                if (nf[0] | nf[1] | nf[2] | nf[3]) {
+                    found = true;
+                    *w = y & ~nf;
                 }
-                if (none || tree) *w = y;
             }
             if (found) odd[turn] = 1;
         };
@@ -537,7 +541,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             if (!whole) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) hide(m, sc[m]);
-                if constexpr (R == 1) clean(at);
+                if (R == 1 && t0 + 32 * NS > s.ctx) clean(at);
             }
             float top[MT];
             bool passed = false;
@@ -588,7 +592,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             const bool whole = t0 + 32 * NS <= s.ctx && t0 + 32 * NS <= t_end && [&] {
                 bool all = true;
 #pragma unroll
-                for (int k = 0; k < 2 * NS; ++k) all &= own(pa, k) >= 0;
+                for (int k = 0; k < 2 * NS; ++k) all &= pa.p[k] >= 0;
                 return all;
             }();
             if constexpr (R > 1) {
@@ -598,11 +602,8 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 wait_and_meet();
                 const uint32_t next = at == tile0 ? at + NS * L::kBytes : tile0;
                 fetch(t0 + STEP, pb, next, 0, NC);
-                bool none = false;
-#pragma unroll
-                for (int i = 0; i < NP; ++i) none |= pa.p[i] < 0;
-                if (tb + STEP > s.ctx || tb + STEP > t_end || none) {  // alike in all waves
-                    if (!whole) clean(at);  // each wave a share of its tiles, before any of them is read
+                if (tb + STEP > s.ctx) {  // alike in all waves
+                    clean(at);            // each wave a share of its tiles, before any of them is read
                     wait_and_meet();
                 }
                 if (t0 < t_end) step(at, whole);
@@ -622,7 +623,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             pa = pb;
             pb = pc;
             pc = pd;
-            pd = pages_at(tb + 4 * STEP);  // asked for steps before the transfers need it
+            pd = pages_at(t0 + 3 * STEP);  // asked for steps before the transfers need it
         }
         wait_loads<0>();  // what was fetched beyond the end
 
@@ -725,9 +726,9 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int b = blockIdx.x / a.c.heads, h = blockIdx.x - b * a.c.heads;
     const int r = WAVES == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave;
-    const int* head = reinterpret_cast<const int*>(a.ws + a.max_items * rb * (D + 2));
+    const ScalarWord* head = scalar_words(reinterpret_cast<const int*>(a.ws + a.max_items * rb * (D + 2)));
     const int chunk = head[0], before = head[1 + b];
-    const Seq s = seq_of(a, b);
+    const Seq s = seq_at(a, b);
     const Plan p = plan_of(a, s, rb, chunk);
     if (p.splits <= 1 || r >= s.n * a.group) return;
     const int blk = r / rb, rl = r - blk * rb;
@@ -756,11 +757,20 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
         l = l * f + lk;
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] *= f;
-        for (int k = 0; k < count; ++k) {
-            const float* y = piece_rows(a, first + (k0 + k * WAVES) * p.blocks, rb, D) + rl * D + lane * N;
-            const float w = __shfl(g, k);
+        for (int k = 0; k < count; k += 8) {  // eight rows requested at a time
+            float y[8][N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) o[e] = fmaf(y[e], w, o[e]);
+            for (int i = 0; i < 8; ++i) {
+                const float* from = piece_rows(a, first + (k0 + min(k + i, count - 1) * WAVES) * p.blocks, rb, D) + rl * D + lane * N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[i][e] = from[e];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = __shfl(g, (k + i) & 63);
+#pragma unroll
+                for (int e = 0; e < N; ++e) o[e] = k + i < count ? fmaf(y[i][e], w, o[e]) : o[e];
+            }
         }
     }
     if constexpr (WAVES == 4) {

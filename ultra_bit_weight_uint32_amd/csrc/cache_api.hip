@@ -85,8 +85,7 @@ int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_hea
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return UBW_EUNSUPPORTED;
     if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || heads > 65536 || kv_heads > 4096 || heads / kv_heads > 1024)
         return UBW_ERANGE;
-    const int64_t rows = (int64_t)max_tree * (heads / kv_heads);
-    *out = (size_t)attn_workspace_floats(batch, rows, kv_heads, head_dim, attn_tile(rows, head_dim)) * 4;
+    *out = (size_t)attn_workspace_floats(batch, max_tree, heads / kv_heads, kv_heads, head_dim) * 4;
     return UBW_OK;
 }
 

@@ -124,9 +124,17 @@ inline int64_t attn_max_items(int batch, int64_t max_rows, int kv_heads, int hea
     return attn_target(t, head_dim) + (int64_t)batch * cdiv(max_rows, attn_rows(t)) * kv_heads;
 }
 // Scratch floats: each piece's rows (head_dim sums, then the running maximum and the sum of weights),
-// then the cut itself (units per piece, each sequence's first piece).
-inline int64_t attn_workspace_floats(int batch, int64_t max_rows, int kv_heads, int head_dim, AttnTile t) {
-    return attn_max_items(batch, max_rows, kv_heads, head_dim, t) * attn_rows(t) * (head_dim + 2) + batch + 1;
+// then the cut itself (units per piece, each sequence's first piece); for trees of max_tree tokens or
+// fewer, whose pieces have other sizes.
+inline int64_t attn_workspace_floats(int batch, int max_tree, int group, int kv_heads, int head_dim) {
+    int64_t most = 0;
+    for (int n = 1; n <= max_tree; ++n) {
+        const int64_t rows = (int64_t)n * group;
+        const AttnTile t = attn_tile(rows, head_dim);
+        const int64_t x = attn_max_items(batch, rows, kv_heads, head_dim, t) * attn_rows(t) * (head_dim + 2);
+        most = x > most ? x : most;
+    }
+    return most + batch + 1;
 }
 
 }  // namespace cache
