@@ -104,13 +104,16 @@ inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
 // How many pieces a batch is aimed to have: about three for each workgroup that is resident with one row
 // wave, one with more (their sums are larger).
 inline int attn_target(AttnTile t, int head_dim) { return t.row_waves == 1 ? 1536 : head_dim == 64 ? 768 : 512; }
+constexpr int kAttnMostChunk = 1 << 25;  // more than the units of 2^31 positions
 UBW_HD inline int attn_chunk(int64_t total_units, int target) {
     const int64_t c = (total_units + target - 1) / target;
-    return (int)(c < 1 ? 1 : c);
+    return (int)(c < 1 ? 1 : c < kAttnMostChunk ? c : kAttnMostChunk);
 }
+// (Where even whole sequences are more pieces than the target it would grow without end.)
 UBW_HD inline int attn_larger_chunk(int chunk, int64_t pieces, int target) {
     const int64_t c = (chunk * pieces + target - 1) / target;
-    return (int)(c > chunk ? c : chunk + 1);
+    const int64_t next = c > chunk ? c : chunk + (int64_t)1;
+    return (int)(next < kAttnMostChunk ? next : kAttnMostChunk);
 }
 UBW_HD inline int attn_splits(int units, int chunk) { return units == 0 ? 0 : (units + chunk - 1) / chunk; }
 UBW_HD inline void attn_range(int units, int splits, int s, int* u0, int* u1) {
