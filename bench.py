@@ -39,7 +39,8 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--configs", action="store_true",
                     help="instead of the headline line: time every GEMV and layer of the 7B MLP and the "
-                         "70B layer at their batches, the group-scale variant, the offline fit and the saliency search")
+                         "70B layer at their batches, the 70B layer's attention block, the group-scale variant, the "
+                         "offline fit and the saliency search")
     ap.add_argument("--profile-shape", type=str, default=None, metavar="N,K,NB,B",
                     help="instead of the headline line: run `--steps` cold ubw_lut_gemv calls of an N x K GEMV with "
                          "NB bases at batch B (no refinement), for counter collection under rocprofv3")
@@ -91,6 +92,7 @@ def main():
         small_sweep(torch, ubw, dev)
         load_time_sweep(torch, ubw, dev)
         config_sweep(torch, ubw, dev)
+        attention_block_sweep(torch, ubw, dev)
         gs_sweep(torch, ubw, dev)
         fit_sweep(torch, ubw, dev)
         saliency_sweep(torch, ubw, dev)
@@ -435,6 +437,84 @@ def config_sweep(torch, ubw, dev):
             torch.cuda.empty_cache()
         del base
         torch.cuda.empty_cache()
+
+
+def attention_block_sweep(torch, ubw, dev):
+    """The attention block of the 70B layer as a decoding step runs it: the grouped q, k, v products, norm and
+    rotation into the paged cache, attention over the context (one token, or a tree of 16 drafted ones), the
+    o product. Weights and cache rotate through at least COLD_BYTES; one JSON line per context and batch,
+    with the two calls between the products timed alone beside the whole."""
+    from workloads import decoder_layer_70b
+
+    def t(a):
+        a = np.ascontiguousarray(a)
+        return torch.from_numpy(a.view(np.int32) if a.dtype == np.uint32 else a).to(dev)
+
+    wl = decoder_layer_70b(seed=0)
+    at, gs = wl.attention, {g.name: g for g in wl.gemvs}
+    w = {nm: dict(packed=ubw.pack_bases(t(g.bits), g.nb, g.n, g.k), alpha_r=t(g.alpha_r), alpha_c=t(g.alpha_c), n=g.n,
+                  idx=t(g.idx), packed_s=ubw.pack_bases(t(g.bits_s), g.ns, g.n, g.s), alpha_r_s=t(g.alpha_r_s),
+                  alpha_c_s=t(g.alpha_c_s), workspace=ubw.workspace(g.n, dev)) for nm, g in gs.items() if nm in "qkvo"}
+    x = t(gs["q"].x)
+    del wl
+    size = sum(v.numel() * v.element_size() for d in w.values() for v in d.values() if torch.is_tensor(v))
+    copies = [{nm: {k: v.clone() if torch.is_tensor(v) else v for k, v in d.items()} for nm, d in w.items()}
+              for _ in range(max(2, -(-COLD_BYTES // size)))]
+    freq = (10000.0 ** (-torch.arange(0, at.head_dim, 2, device=dev, dtype=torch.float64) / at.head_dim)).float()
+    for ctx in at.contexts:
+        for b in (1, 16):
+            pages = -(-(ctx + b) // at.page_size)
+            per = 4 * pages * at.page_size * at.kv_heads * at.head_dim
+            caches = []
+            for _ in range(max(2, -(-COLD_BYTES // per))):
+                shape = (pages, at.kv_heads, at.page_size, at.head_dim)
+                caches.append(ubw.KVCache(*(torch.randn(shape, device=dev, dtype=torch.float16) for _ in "kv")))
+            i32 = dict(dtype=torch.int32, device=dev)
+            table = torch.randperm(pages, **i32).view(1, -1)
+            slots = torch.tensor([int(table[0, p // at.page_size]) * at.page_size + p % at.page_size
+                                  for p in range(ctx, ctx + b)], **i32)
+            # a binary tree of drafted tokens: token i hangs on token (i - 1) / 2
+            up = [[0]]
+            for i in range(1, b):
+                up.append(up[(i - 1) // 2] + [i])
+            masks = torch.tensor([sum(1 << j for j in u) for u in up], dtype=torch.int64, device=dev)
+            pos = torch.tensor([ctx + len(u) - 1 for u in up], **i32)
+            start, length = torch.tensor([0, b], **i32), torch.tensor([ctx], **i32)
+            ws = ubw.tree_attn_workspace(1, b, at.heads, at.kv_heads, at.head_dim, dev)
+            ys = {nm: torch.empty((b, gs[nm].n), device=dev) for nm in "qkvo"}
+            heads = {nm: ys[nm].view(b, -1, at.head_dim) for nm in "qkv"}
+            qr = torch.empty((b, at.heads, at.head_dim), dtype=torch.float16, device=dev)
+            o = torch.empty_like(qr)
+
+            def between(i):
+                c = caches[i % len(caches)]
+                ubw.qk_norm_rope(heads["q"], heads["k"], heads["v"], c, pos, slots, freq, out=qr)
+                ubw.tree_attn(qr, c, table, start, length, masks, max_tree=b, max_len=ctx + b, out=o, workspace=ws)
+
+            def block(i):
+                d = copies[i % len(copies)]
+                ubw.lut_gemv_multi([d[nm] | dict(y=ys[nm]) for nm in "qkv"], x[:b], gs["q"].k)
+                between(i)
+                g, e = gs["o"], d["o"]
+                ubw.lut_gemv_refined(e["packed"], e["alpha_r"], e["alpha_c"], e["idx"], e["packed_s"], e["alpha_r_s"],
+                                     e["alpha_c_s"], o.view(b, -1), g.n, g.k, y=ys["o"], workspace=e["workspace"])
+
+            us = {}
+            for name, fn in (("block", block), ("between", between)):
+                for i in range(max(len(copies), len(caches))):
+                    fn(i)
+                us[name] = run_queued(torch, fn, 50) * 1e3 / 50
+            if not torch.isfinite(ys["o"]).all():
+                raise RuntimeError("attention block: non-finite output")
+            kv_bytes = 4 * (ctx + b) * at.kv_heads * at.head_dim
+            print(json.dumps({"sweep": "70B attention block", "context": ctx, "batch": b, "us": round(us["block"], 2),
+                              "us_norm_rope_attention": round(us["between"], 2), "kv_bytes": kv_bytes,
+                              "kv_GBps_norm_rope_attention": round(kv_bytes / us["between"] / 1e3, 1),
+                              "cold_copies": len(copies), "cold_caches": len(caches)}), flush=True)
+            del caches
+            torch.cuda.empty_cache()
+    del copies, w
+    torch.cuda.empty_cache()
 
 
 def profile_shape(torch, ubw, dev, spec, steps):

@@ -133,6 +133,16 @@ class TernaryLayer:
 
 
 @dataclass
+class Attention:
+    """What lies between a decoder layer's q, k, v products and its o product."""
+    heads: int
+    kv_heads: int
+    head_dim: int
+    page_size: int = 16
+    contexts: Tuple[int, ...] = ()   # context lengths it is measured at
+
+
+@dataclass
 class Workload:
     name: str
     description: str
@@ -140,6 +150,7 @@ class Workload:
     ternary: List[TernaryLayer] = field(default_factory=list)
     tokens: Optional[np.ndarray] = None   # [T, d] float16 token vectors (ternary stack)
     batches: Tuple[int, ...] = (1,)
+    attention: Optional[Attention] = None
 
 
 def single_gemv_256x512(seed: int = 0) -> Workload:
@@ -183,12 +194,14 @@ def mlp_7b(seed: int = 0) -> Workload:
 
 def decoder_layer_70b(seed: int = 0) -> Workload:
     """70B-shaped decoder layer: q, k, v, o, gate, up, down with 3 bases + 5% salient columns
-    (2 refinement bases), fp16 x, batch 1 and 16 (x drawn at batch 16)."""
+    (2 refinement bases), fp16 x, batch 1 and 16 (x drawn at batch 16); 64 query heads over 8 key/value
+    heads of 128 (8192 = 64 x 128, 1024 = 8 x 128)."""
     rng = np.random.default_rng(seed)
     shapes = (("q", 8192, 8192), ("k", 1024, 8192), ("v", 1024, 8192), ("o", 8192, 8192),
               ("gate", 28672, 8192), ("up", 28672, 8192), ("down", 8192, 28672))
     gs = [make_gemv(rng, nm, n, k, 3, s=salient_count(0.05, k), ns=2, batch=16) for nm, n, k in shapes]
-    return Workload("layer_70b", "70B decoder layer, 7 GEMVs", gs, batches=(1, 16))
+    return Workload("layer_70b", "70B decoder layer, 7 GEMVs", gs, batches=(1, 16),
+                    attention=Attention(64, 8, 128, contexts=(1024, 32768)))
 
 
 WORKLOADS = {f.__name__: f for f in (single_gemv_256x512, ternary_stack_256x768, attn_proj_7b, mlp_7b,
