@@ -30,7 +30,7 @@ static void check_cut(Rng& r) {
         const int tree = (int)rnd(r, 1, UBW_MAX_TREE), batch = (int)rnd(r, 1, it % 5 ? 40 : 600);
         const int64_t max_rows = (int64_t)tree * group;
         const AttnTile t = attn_tile(max_rows, dim);
-        const int rb = attn_rows(t), target = attn_target(t, dim);
+        const int rb = attn_rows(t);
         CHECK(rb >= 16 && (t.row_waves == 1 || t.row_waves == 2 || t.row_waves == 4), "tile %d x %d", t.tiles, t.row_waves);
         if (dim < 256 && max_rows <= 128) CHECK(rb >= max_rows, "%d rows in blocks of %d", (int)max_rows, rb);
         std::vector<int64_t> units(batch), blocks(batch);
@@ -42,6 +42,8 @@ static void check_cut(Rng& r) {
             blocks[b] = cdiv((int64_t)n * group, rb);
             total += units[b] * blocks[b] * kv;
         }
+        const int target = attn_aim(total, attn_target(t, dim), t.row_waves == 1);
+        CHECK(target >= 256 && target <= attn_target(t, dim), "aim %d", target);
         int chunk = attn_chunk(total, target);
         const auto pieces = [&](int c) {
             int64_t p = 0;

@@ -159,7 +159,7 @@ __device__ inline int64_t wg_sum(int64_t x, int64_t* lds) {
 // Cuts the batch: units per piece (the least for which the pieces do not pass the target by more than
 // the sequences that cannot be joined make them), and in pre[b] the pieces of the sequences before b.
 template <int NT>
-__device__ inline int cut_batch(const AttnArgs& a, int rb, int* pre, int64_t* lds) {
+__device__ inline int cut_batch(const AttnArgs& a, int rb, bool one_row_wave, int* pre, int64_t* lds) {
     const int tid = threadIdx.x;
     const int per = (a.batch + NT - 1) / NT;
     const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
@@ -168,7 +168,9 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, int* pre, int64_t* ld
         const Plan p = plan_of(a, seq_of(a, b), rb, 0);
         units += (int64_t)p.units * p.blocks;
     }
-    int chunk = attn_chunk(wg_sum<NT>(units, lds) * a.c.heads, a.target);
+    const int64_t total = wg_sum<NT>(units, lds) * a.c.heads;
+    const int target = attn_aim(total, a.target, one_row_wave);
+    int chunk = attn_chunk(total, target);
     int mine = 0;
     for (int step = 0;; ++step) {
         mine = 0;
@@ -177,8 +179,8 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, int* pre, int64_t* ld
             mine += p.splits * p.blocks * a.c.heads;
         }
         const int64_t pieces = wg_sum<NT>(mine, lds);
-        if (step == 4 || pieces <= a.target) break;
-        chunk = attn_larger_chunk(chunk, pieces, a.target);
+        if (step == 4 || pieces <= target) break;
+        chunk = attn_larger_chunk(chunk, pieces, target);
     }
     int y = mine;
 #pragma unroll
@@ -310,7 +312,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     int chunk = 0, items;
     const int blocks_max = (a.max_tree * a.group + RB - 1) / RB;
     if (a.target > 0) {
-        chunk = cut_batch<C::kThreads>(a, RB, pre, lds64);
+        chunk = cut_batch<C::kThreads>(a, RB, R == 1, pre, lds64);
         items = __builtin_amdgcn_readfirstlane(pre[a.batch]);
         if (blockIdx.x == 0) {  // for k_join
             int* head = reinterpret_cast<int*>(a.ws + a.max_items * RB * (D + 2));

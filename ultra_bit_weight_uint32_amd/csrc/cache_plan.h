@@ -101,9 +101,15 @@ inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
 // How a batch is cut: sequence b has blocks_b row blocks of units_b units of positions for each
 // key/value head; a piece is one block over `chunk` units at most, a sequence's pieces of equal size
 // but for one unit. chunk starts at total / target and grows while there are more pieces than that.
-// How many pieces a batch is aimed to have: about three for each workgroup that is resident with one row
-// wave, one with more (their sums are larger).
+// How many pieces a batch is aimed to have, at most: with one row wave three for each workgroup that is
+// resident, with more one (their sums are larger).
 inline int attn_target(AttnTile t, int head_dim) { return t.row_waves == 1 ? 1536 : head_dim == 64 ? 768 : 512; }
+// ... and for this many units: three a workgroup only where each still has kAttnLong units or more, so
+// that starting a piece costs little beside it.
+constexpr int kAttnLong = 8;
+UBW_HD inline int attn_aim(int64_t total_units, int target, bool one_row_wave) {
+    return one_row_wave && total_units < (int64_t)target * kAttnLong ? target / 3 : target;
+}
 constexpr int kAttnMostChunk = 1 << 25;  // more than the units of 2^31 positions
 UBW_HD inline int attn_chunk(int64_t total_units, int target) {
     const int64_t c = (total_units + target - 1) / target;
