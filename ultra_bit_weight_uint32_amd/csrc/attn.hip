@@ -231,12 +231,16 @@ struct Layout {
 };
 
 // 16 bytes a lane from memory straight to LDS at `lds` + 16 lane. The compiler does not see the
-// transfer: waits are placed by hand.
-template <int OFF>
+// transfer: waits are placed by hand. ONCE: nobody else reads these bytes (keys and values under one row
+// block), they need not stay in the L2 (1.3 GB in 64 ragged sequences: 229 us, 249 without; 0.85 GB under
+// one block of 128 rows 161, 169 without; under four row blocks they are read again: 638 us without, 648
+// with).
+template <bool ONCE>
 __device__ inline void to_lds(Rsrc r, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds" ::"s"(lds), "v"(off), "s"(r),
-                 "n"(OFF)
-                 : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
 }
 template <int N>
 __device__ inline void wait_loads() {  // all but the newest N transfers have arrived
@@ -283,7 +287,7 @@ struct Cfg {
     static constexpr int kSimd = kPerCu * kThreads / 256 < 1 ? 1 : kPerCu * kThreads / 256;
 };
 
-template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB>
+template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>
 __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8, D, MT, R, T, NS, NB>::kSimd)) void k_attn(AttnArgs a) {
     using H = Half<TQ>;
     using L = Layout<FP8, D>;
@@ -404,13 +408,13 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     if (ch < L::CK) {
                         const int sub = ch / L::KL, piece = ch % L::KL;
                         const int page = sub ? pg.p[2 * n + 1] : pg.p[2 * n], x = t + 32 * n + 16 * sub;
-                        to_lds<0>(rows16(kb + (page < 0 ? 0 : page) * a.c.k_page + (int64_t)(x & pmask) * a.c.k_row + piece * 64,
+                        to_lds<ONCE>(rows16(kb + (page < 0 ? 0 : page) * a.c.k_page + (int64_t)(x & pmask) * a.c.k_row + piece * 64,
                                          page < 0 ? 0u : min(16, t_end - x) * a.c.k_row - piece * 64), koff, to);
                     } else {
                         const int row = (ch - L::CK) * L::RP, sub = row >> 4;  // of the tile
                         const int page = sub ? pg.p[2 * n + 1] : pg.p[2 * n], x = t + 32 * n + row;
                         const uint32_t off = (uint32_t)vt * a.c.v_row + (uint32_t)((vp ^ L::mix((row + vt) & 15)) * 16);
-                        to_lds<0>(rows16(vb + (page < 0 ? 0 : page) * a.c.v_page + (int64_t)(x & pmask) * a.c.v_row,
+                        to_lds<ONCE>(rows16(vb + (page < 0 ? 0 : page) * a.c.v_page + (int64_t)(x & pmask) * a.c.v_row,
                                          page < 0 ? 0u : min(L::RP, max(t_end - x, 0)) * a.c.v_row), off, to);
                     }
                 }
@@ -806,14 +810,14 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     if (a.lse && lane == 0) a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
-template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB>
+template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
     using C = Cfg<FP8, D, MT, R, T, NS, NB>;
     const int64_t rows = (int64_t)a.max_tree * a.group, pairs = (int64_t)a.batch * a.c.heads;
     const int64_t most = a.target > 0 ? a.max_items : pairs * cdiv(rows, C::RB);
     const int64_t wgs = most < kCus * C::kPerCu ? cdiv(most, 8) * 8 : kCus * C::kPerCu;
     const unsigned lds = a.target > 0 ? (unsigned)(a.batch + 1) * 4 : 0;
-    k_attn<TQ, FP8, D, MT, R, T, NS, NB><<<(unsigned)wgs, C::kThreads, lds, s>>>(a);
+    k_attn<TQ, FP8, D, MT, R, T, NS, NB, ONCE><<<(unsigned)wgs, C::kThreads, lds, s>>>(a);
     if (a.target > 0) {
         // few rows: many pieces each, four waves share them
         if (rows * pairs <= 1024)
@@ -825,13 +829,16 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
 }
 template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const AttnArgs& a, AttnTile t, hipStream_t s) {
+    const bool one_block = a.max_tree * a.group <= attn_rows(t);
     if constexpr (D == 256) {
-        return t.row_waves == 1 ? launch<TQ, FP8, D, 1, 1, 2, 1, 2>(a, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2>(a, s);
+        if (t.row_waves == 1) return launch<TQ, FP8, D, 1, 1, 2, 1, 2, true>(a, s);
+        return one_block ? launch<TQ, FP8, D, 1, 4, 1, 1, 2, true>(a, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2, false>(a, s);
     } else {
-        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1, 4, 1, (FP8 || D == 64) ? 2 : 1>(a, s);
-        return t.row_waves == 1   ? launch<TQ, FP8, D, 2, 1, 4, 1, (FP8 || D == 64) ? 2 : 1>(a, s)
-               : t.row_waves == 2 ? launch<TQ, FP8, D, 2, 2, 2, 1, 2>(a, s)
-                                  : launch<TQ, FP8, D, 2, 4, 1, 2, 2>(a, s);
+        constexpr int NB = FP8 || D == 64 ? 2 : 1;
+        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1, 4, 1, NB, true>(a, s);
+        if (t.row_waves == 1) return launch<TQ, FP8, D, 2, 1, 4, 1, NB, true>(a, s);
+        if (t.row_waves == 2) return launch<TQ, FP8, D, 2, 2, 2, 1, 2, true>(a, s);
+        return one_block ? launch<TQ, FP8, D, 2, 4, 1, 2, 2, true>(a, s) : launch<TQ, FP8, D, 2, 4, 1, 2, 2, false>(a, s);
     }
 }
 template <typename TQ, bool FP8>

@@ -8,7 +8,8 @@
 // a token are computed once per workgroup into LDS: the angle is position * inv_freq in fp64, reduced
 // to a fraction of a turn there (at position 10^6 an fp32 angle would be off by 0.03), and only the
 // fraction goes to fp32.
-// Bound: HBM for prompts, launch and memory latency for a few tokens.
+// Bound: HBM for prompts (319 MB read and written in 69 us, 4.6 TB/s; a plain copy of this card reaches
+// 4.9), launch and memory latency for a few tokens (3.3 us for one).
 #include "cache_internal.h"
 
 namespace ubw {
@@ -182,7 +183,7 @@ template <typename TI, int D>
 hipError_t launch(const RopeArgs& a, bool pairs, hipStream_t s) {
     const int all = a.heads + 2 * a.c.heads;
     // One pass of 16 heads per workgroup while there are few, else all heads of a token, its angles
-    // computed once.
+    // computed once (8191 tokens of 80 heads: 69 us, 77 with 32 heads a workgroup, 87 with 16).
     const int per = (int64_t)a.tokens * cdiv(all, 16) <= 2048 ? 16 : (int)cdiv(all, 16) * 16;
     const dim3 grid(a.tokens, (unsigned)cdiv(all, per));
     if (pairs)
