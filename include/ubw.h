@@ -514,7 +514,8 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
  * are cut as above. tokens = 0 or batch = 0 enqueues nothing.
  * Errors: UBW_EINVAL (null, sizes, heads no multiple of kv_heads, scale not positive and finite),
  *         UBW_EUNSUPPORTED (types, head_dim, page_size), UBW_ERANGE (batch above UBW_MAX_SEQS,
- *         max_tree, strides, 1024 query heads per key/value head, 2^24 pieces of work), UBW_EALIGN, UBW_ESIZE (workspace), UBW_EHIP.
+ *         max_tree, strides, 1024 query heads per key/value head, table_cols * page_size above 2^30,
+ *         2^24 pieces of work), UBW_EALIGN (rows 16 bytes, masks 8, int32 and fp32 arrays 4), UBW_ESIZE (workspace), UBW_EHIP.
  */
 int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_heads, int head_dim, size_t* out);
 int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
@@ -573,7 +574,8 @@ typedef struct ubw_page_pool {
 } ubw_page_pool;
 
 /* An empty pool: every page free, every sequence without pages, status 0.
- * Errors: UBW_EINVAL (null, sizes), UBW_EUNSUPPORTED (page_size), UBW_ERANGE, UBW_EHIP. */
+ * Errors (of all four calls): UBW_EINVAL (null, sizes), UBW_EUNSUPPORTED (page_size), UBW_ERANGE,
+ * UBW_EALIGN (an array not 4-byte aligned), UBW_EHIP. */
 int ubw_pages_init(const ubw_page_pool* pool, void* stream);
 
 /*

@@ -173,3 +173,23 @@ def test_pool_calls_refuse_null():
     assert L.ubw_pages_fork(p, None, None) == EINVAL
     assert L.ubw_pages_reserve(p, None, FAKE, None) == EINVAL
     assert L.ubw_pages_reserve(p, FAKE, None, None) == EINVAL
+
+
+@pytest.mark.parametrize("call,kw", [
+    (rope, dict(pos=FAKE + 2)), (rope, dict(slots=FAKE + 1)), (rope, dict(freq=FAKE + 2)), (attn, dict(start=FAKE + 2)),
+    (attn, dict(ctx=FAKE + 1)), (attn, dict(table=FAKE + 3)), (copy, dict(pairs=FAKE + 2)), (compact, dict(table=FAKE + 2)),
+    (compact, dict(ctx=FAKE + 2)), (compact, dict(keep=FAKE + 2)),
+])
+def test_arrays_are_aligned(call, kw):
+    assert call(**kw) == EALIGN
+
+
+@pytest.mark.parametrize("field", ["ref", "free_bits", "table", "held", "len", "status"])
+def test_pool_arrays_are_aligned(field):
+    p = ctypes.byref(ubw.PagePoolDesc(**(POOL | {field: FAKE + 2})))
+    assert ubw.lib().ubw_pages_init(p, None) == EALIGN
+    assert ubw.lib().ubw_pages_trim(p, FAKE, None) == EALIGN
+
+
+def test_attention_positions_stay_clear_of_32_bits():
+    assert attn(cols=(1 << 26) + 1, ld_table=1 << 27) == ERANGE

@@ -420,6 +420,22 @@ def test_attention_scores_of_every_size():
             attend_and_check(q, cache, table, [0, 1], [n], None, scale=1.0, split=split)
 
 
+def test_attention_of_scores_near_the_lowest_number():
+    """A lone position weighs 1 however low its score is, and of two far ones the higher takes all."""
+    cache = cache_of(1, 1, 16, 64, BF16, gen(18))
+    cache.k.zero_()
+    q = torch.zeros((2, 2, 64), dtype=BF16, device=DEV)
+    q[..., 0] = 1e19
+    cache.k[0, 0, :2, 0] = torch.tensor([-1e19, -2e19], device=DEV)
+    table = i32([[0]])
+    for split in (True, False):
+        ws = ubw.tree_attn_workspace(1, 2, 2, 1, 64, DEV) if split else None
+        lse = torch.empty((2, 2), device=DEV)
+        out = ubw.tree_attn(q, cache, table, i32([0, 2]), i32([0]), max_tree=2, scale=1.0, lse=lse, workspace=ws)
+        assert torch.equal(out, cache.v[0, 0, 0].expand_as(out))
+        assert torch.allclose(lse, torch.full_like(lse, float(q[0, 0, 0].double() * cache.k[0, 0, 0, 0].double())), rtol=1e-6)
+
+
 def test_attention_cuts_what_it_cannot_use():
     """Lengths beyond the table, entries that are no pages, negative contexts, rows of no sequence, trees
     over max_tree: cut as documented, the rest right, nothing else written."""
@@ -696,6 +712,19 @@ def test_pool_hands_out_everything_and_refuses_more():
     ubw.pages_reserve(pool, i32(big))
     model.reserve(big)
     model.check(pool)
+
+
+def test_pool_bits_past_the_last_page_are_no_pages():
+    pool = ubw.page_pool(40, 16, 2, 64, DEV)
+    guard = torch.full((64,), 7, dtype=torch.int32, device=DEV)
+    wide = torch.cat((pool.ref, guard))   # counts behind the last page, never written
+    pool = ubw.PagePool(wide[:40], pool.free, pool.table, pool.held, pool.len, pool.status, 16)
+    pool.free.fill_(-1)
+    ubw.pages_reserve(pool, i32([16 * 40, 0]))
+    assert pool.held.tolist() == [40, 0] and pool.status.item() == 0
+    ubw.pages_reserve(pool, i32([0, 1]))
+    assert pool.status.item() == ubw.PagePool.NO_PAGES
+    assert (wide[40:] == 7).all() and (wide[:40] == 1).all()
 
 
 # ---------------------------------------------------------------------------------------------

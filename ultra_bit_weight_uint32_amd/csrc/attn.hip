@@ -14,10 +14,12 @@
 //     operand's k index counts positions in that order. For A, transposing LDS reads give lane (dim, j)
 //     the same eight positions of its dim; value rows lie with their 16-byte columns exchanged by XOR so
 //     that these reads spread over the banks. 8-bit values are read so too and widened on the way.
-//   * m is not followed exactly: o is scaled only when a score passes m + 15 (a wave-uniform branch
-//     that long contexts take a few times), so the usual step has no cross-lane work at all, l is kept
-//     per lane, and p stays below 2^15, inside fp16. m starts 7 below the maximum, so that weights down
-//     to 2^-21 of the largest are normal fp16 numbers.
+//   * m is not followed exactly: o is scaled only when a score passes m by more than 2^8 (a wave-uniform
+//     branch that long contexts take a few times), so the usual step has no cross-lane work at all, l is
+//     kept per lane, and p = 2^((s - m) log2 e + 7) stays below 2^15, inside fp16, while weights down to
+//     2^-21 of the largest are normal fp16 numbers. m is kept as a score and -m is what the product K Q^T
+//     starts from, so that s - m costs nothing and is right at any size of s (s log2 e - m in one fused
+//     step, m rounded, is off by the rounding of m: at |s| = 10^8 the largest weight would be 2^(7 +- 4)).
 // Descriptors cover 16 rows; one of size 0 stands for rows that are not needed or on no valid page, so
 // every step issues the same transfers, their count is waited for exactly, and no table entry is ever
 // trusted. Few rows (R = 1): each wave has tiles of its own and no barrier; with one tile, its keys make
@@ -86,11 +88,9 @@ __device__ inline uint32_t pack(float a, float b) {  // rounded to nearest even
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLow = -1e30f;     // m of a row that has seen nothing: 2^(-inf - kLow) = 0
+constexpr float kLow = -3.402823466e38f;  // m of a row that has seen nothing
 constexpr float kShift = 7.f, kSlack = 8.f;
-
 constexpr int kCus = 256;
-
 // Words that no kernel running beside this one writes, read by the scalar unit. (As vector loads they
 // would be waited for behind all transfers under way.)
 typedef const __attribute__((address_space(4))) int32_t ScalarWord;
@@ -231,7 +231,7 @@ struct Layout {
 };
 
 // 16 bytes a lane from memory straight to LDS at `lds` + 16 lane. The compiler does not see the
-// transfer: waits are placed by hand. ONCE: nobody else reads these bytes (keys and values under one row
+// transfer: waits are placed by hand (m0 it sets itself wherever it uses it). ONCE: nobody else reads these bytes (keys and values under one row
 // block), they need not stay in the L2 (1.3 GB in 64 ragged sequences: 229 us, 249 without; 0.85 GB under
 // one block of 128 rows 161, 169 without; under four row blocks they are read again: 638 us without, 648
 // with).
@@ -462,11 +462,13 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         }
 
         f32x4 o[MT][NE];
-        float mx[MT], l[MT];
+        float ms[MT], lim[MT], l[MT];
+        f32x4 less[MT];  // -ms
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            mx[m] = kLow;
-            l[m] = 0.f;
+            ms[m] = l[m] = 0.f;
+            lim[m] = kLow;
+            less[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < NE; ++e) o[m][e] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
@@ -490,7 +492,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
 #pragma unroll
             for (int sub = 0; sub < 2 * NS; ++sub) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) sc[m][sub] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int m = 0; m < MT; ++m) sc[m][sub] = less[m];
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t from = at + (sub >> 1) * L::kBytes + (sub & 1) * L::KL * 1024 + lane * 16;
@@ -556,19 +558,24 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 top[m] = sc[m][0][0];
 #pragma unroll
                 for (int k = 1; k < 8 * NS; ++k) top[m] = fmaxf(top[m], sc[m][k >> 2][k & 3]);
-                passed |= fmaf(top[m], cc, -mx[m]) > kShift + kSlack;
+                passed |= top[m] > lim[m];
             }
             if (__any(passed)) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     float x = fmaxf(top[m], __shfl_xor(top[m], 16));
                     x = fmaxf(x, __shfl_xor(x, 32));
-                    const float to = fmaxf(mx[m], fmaf(x, cc, -kShift));
-                    const float f = __builtin_amdgcn_exp2f(mx[m] - to);
-                    mx[m] = to;
+                    const bool first = lim[m] == kLow;  // the row has seen nothing yet: o and l are 0
+                    if (!(first ? x > -INFINITY : x > 0.f)) x = 0.f;
+                    else lim[m] = kSlack / cc;
+                    const float f = first ? 1.f : __builtin_amdgcn_exp2f(-x * cc);
+                    ms[m] += x;
+                    less[m] = f32x4{-ms[m], -ms[m], -ms[m], -ms[m]};
                     l[m] *= f;
 #pragma unroll
                     for (int e = 0; e < NE; ++e) o[m][e] *= f;
+#pragma unroll
+                    for (int k = 0; k < 8 * NS; ++k) sc[m][k >> 2][k & 3] -= x;
                 }
             }
             u32x4 pf[MT][NS];
@@ -579,7 +586,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     float pr[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        pr[k] = __builtin_amdgcn_exp2f(fmaf(sc[m][2 * n + (k >> 2)][k & 3], cc, -mx[m]));
+                        pr[k] = __builtin_amdgcn_exp2f(fmaf(sc[m][2 * n + (k >> 2)][k & 3], cc, kShift));
                         l[m] += pr[k];
                     }
                     pf[m][n] = u32x4{pack<TQ>(pr[0], pr[1]), pack<TQ>(pr[2], pr[3]), pack<TQ>(pr[4], pr[5]), pack<TQ>(pr[6], pr[7])};
@@ -632,6 +639,11 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             pd = pages_at(t0 + 3 * STEP);  // asked for steps before the transfers need it
         }
         wait_loads<0>();  // what was fetched beyond the end
+
+        // From here on the maximum in units of log2, with the shift: weights are 2^(s log2 e - mx).
+        float mx[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) mx[m] = lim[m] == kLow ? kLow : fmaxf(fmaf(ms[m], cc, -kShift), kLow);
 
         // Join the T waves of each row over positions: every one brings its rows to the common maximum, the
         // first adds up. Lane (c, j) has row c, dims 16 e + 4 j .. + 3.

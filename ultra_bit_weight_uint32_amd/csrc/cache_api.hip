@@ -25,6 +25,7 @@ ubw_kv_cache with_used_strides(const ubw_kv_cache& c) {
 
 int check_table(const int32_t* table, int64_t ld, int cols) {
     if (!table || cols < 1 || ld < cols) return UBW_EINVAL;
+    if (!aligned4(table)) return UBW_EALIGN;
     if (cols > (1 << 24) || ld > ((int64_t)1 << 40)) return UBW_ERANGE;
     return UBW_OK;
 }
@@ -55,7 +56,8 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
         (st = check_rows(v, ldv, tokens, c.kv_heads, d, size)) != UBW_OK ||
         (st = check_rows(q_out, ldo, tokens, heads, d, 2)) != UBW_OK)
         return st;
-    if (!aligned16(q_weight) || !aligned16(k_weight)) return UBW_EALIGN;
+    if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned4(inv_freq) || !aligned4(positions) || !aligned4(slots))
+        return UBW_EALIGN;
     RopeArgs a{};
     a.c = pages_of(c);
     a.q = q;
@@ -105,11 +107,11 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     if (tokens == 0 || batch == 0) return UBW_OK;
     if (!q_start || !ctx_len) return UBW_EINVAL;
     if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
-    if ((int64_t)table_cols * c.page_size > 0x7ffffff0) return UBW_ERANGE;
+    if ((int64_t)table_cols * c.page_size > (1 << 30)) return UBW_ERANGE;  // positions stay clear of 2^31
     if ((st = check_rows(q, ldq, tokens, heads, c.head_dim, 2)) != UBW_OK ||
         (st = check_rows(out, ldo, tokens, heads, c.head_dim, 2)) != UBW_OK)
         return st;
-    if ((reinterpret_cast<uintptr_t>(masks) & 7) || (reinterpret_cast<uintptr_t>(lse) & 3)) return UBW_EALIGN;
+    if ((reinterpret_cast<uintptr_t>(masks) & 7) || !aligned4(lse) || !aligned4(q_start) || !aligned4(ctx_len)) return UBW_EALIGN;
     size_t need = 0;
     if ((st = ubw_tree_attn_workspace_bytes(batch, max_tree, heads, c.kv_heads, c.head_dim, &need)) != UBW_OK) return st;
     if (!workspace && ws_bytes != 0) return UBW_EINVAL;
@@ -153,6 +155,7 @@ int ubw_cache_copy_pages(const ubw_kv_cache* cache, const int32_t* pairs, int64_
     if (count > (1 << 20) || copy_grid(c) > kMaxGrid) return UBW_ERANGE;
     if (count == 0) return UBW_OK;
     if (!pairs) return UBW_EINVAL;
+    if (!aligned4(pairs)) return UBW_EALIGN;
     return hip_status(launch_copy_pages(pages_of(c), c.layers, c.page_size, c.head_dim * type_size(c.dtype), pairs,
                                         (int)count, as_stream(stream)));
 }
@@ -166,6 +169,7 @@ int ubw_cache_compact(const ubw_kv_cache* cache, const int32_t* table, int64_t l
     if (batch > UBW_MAX_SEQS || width > 1024 || compact_grid(c) > kMaxGrid) return UBW_ERANGE;
     if (batch == 0 || width == 0) return UBW_OK;
     if (!ctx_len || !keep) return UBW_EINVAL;
+    if (!aligned4(ctx_len) || !aligned4(keep)) return UBW_EALIGN;
     if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
     return hip_status(launch_compact(pages_of(c), c.layers, c.head_dim * type_size(c.dtype), table, ld_table, table_cols,
                                      ctx_len, keep, width, batch, as_stream(stream)));
@@ -180,6 +184,7 @@ int ubw_pages_trim(const ubw_page_pool* pool, const int32_t* new_len, void* stre
     const int st = check_pool(pool);
     if (st != UBW_OK) return st;
     if (!new_len) return UBW_EINVAL;
+    if (!aligned4(new_len)) return UBW_EALIGN;
     return hip_status(launch_pages_trim(*pool, new_len, as_stream(stream)));
 }
 
@@ -187,6 +192,7 @@ int ubw_pages_fork(const ubw_page_pool* pool, const int32_t* parents, void* stre
     const int st = check_pool(pool);
     if (st != UBW_OK) return st;
     if (!parents) return UBW_EINVAL;
+    if (!aligned4(parents)) return UBW_EALIGN;
     return hip_status(launch_pages_fork(*pool, parents, as_stream(stream)));
 }
 
@@ -194,6 +200,7 @@ int ubw_pages_reserve(const ubw_page_pool* pool, const int32_t* room, int32_t* p
     const int st = check_pool(pool);
     if (st != UBW_OK) return st;
     if (!room || !pairs) return UBW_EINVAL;
+    if (!aligned4(room) || !aligned4(pairs)) return UBW_EALIGN;
     return hip_status(launch_pages_reserve(*pool, room, pairs, as_stream(stream)));
 }
 

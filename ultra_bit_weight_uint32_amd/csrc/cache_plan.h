@@ -20,6 +20,7 @@ constexpr int64_t kMaxGrid = (1 << 24) - 1;
 constexpr int kCopyVecs = 4;  // 16-byte vectors a copying thread has in flight
 
 inline bool page_size_ok(int ps) { return ps >= 16 && ps <= 1024 && (ps & (ps - 1)) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline int log2_of(int pow2) {
     int l = 0;
     while ((1 << l) < pow2) ++l;
@@ -48,7 +49,7 @@ inline int check_cache(const ubw_kv_cache* c) {
     if (!page_size_ok(c->page_size)) return UBW_EUNSUPPORTED;
     if (c->pages > (1 << 24) || c->kv_heads > 4096 || c->layers > 65536) return UBW_ERANGE;
     if ((int64_t)c->pages * c->page_size > 0x7fffffff) return UBW_ERANGE;  // slots are int32
-    if (!aligned16(c->k) || !aligned16(c->v)) return UBW_EALIGN;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale)) return UBW_EALIGN;
     const int size = type_size(c->dtype);
     int st = check_strides(c->k_stride, *c, size);
     return st != UBW_OK ? st : check_strides(c->v_stride, *c, size);
@@ -77,6 +78,9 @@ inline int check_pool(const ubw_page_pool* p) {
     if (!page_size_ok(p->page_size)) return UBW_EUNSUPPORTED;
     if (p->pages > (1 << 24) || p->seqs > UBW_MAX_SEQS || p->max_pages > (1 << 24)) return UBW_ERANGE;
     if ((int64_t)p->max_pages * p->page_size > 0x7fffffff) return UBW_ERANGE;  // lengths are int32
+    if (!aligned4(p->ref) || !aligned4(p->free_bits) || !aligned4(p->table) || !aligned4(p->held) || !aligned4(p->len) ||
+        !aligned4(p->status))
+        return UBW_EALIGN;
     return UBW_OK;
 }
 

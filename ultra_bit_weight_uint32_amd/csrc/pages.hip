@@ -262,8 +262,12 @@ __global__ __launch_bounds__(1024) void k_pages_reserve(ubw_page_pool p, int lps
     // free pages: this thread's words, and how many lie before them
     const int words = (p.pages + 31) >> 5, per = (words + 1023) >> 10;
     const int w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    const auto free_of = [&](int w) {  // bits past the last page are no pages, whatever they hold
+        const int past = p.pages - w * 32;
+        return p.free_bits[w] & (past >= 32 ? ~0u : (1u << past) - 1);
+    };
     int have = 0;
-    for (int w = w0; w < w1; ++w) have += __popc(p.free_bits[w]);
+    for (int w = w0; w < w1; ++w) have += __popc(free_of(w));
     int64_t all;
     int rank = (int)wg_prefix(have, lds, &all);  // its barriers also publish before[] and holds[]
     if (total > all) {
@@ -271,13 +275,13 @@ __global__ __launch_bounds__(1024) void k_pages_reserve(ubw_page_pool p, int lps
         return;
     }
     int w = w0;
-    uint32_t bits = w < w1 ? p.free_bits[w] : 0u, left = bits;
+    uint32_t bits = w < w1 ? free_of(w) : 0u, left = bits;
     for (int r0 = 0; r0 < total; r0 += kWindow) {
         const int r1 = (int)min((int64_t)r0 + kWindow, total);
         while (w < w1 && rank < r1) {  // this thread's pages of the window
             if (!left) {
                 if (left != bits) p.free_bits[w] = left;
-                bits = left = ++w < w1 ? p.free_bits[w] : 0u;
+                bits = left = ++w < w1 ? free_of(w) : 0u;
                 continue;
             }
             list[rank - r0] = w * 32 + __ffs((int)left) - 1;
