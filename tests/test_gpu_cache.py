@@ -293,6 +293,11 @@ ATTEND = [  # heads, kv, dim, q type, cache type, page, contexts, tokens, masks
     (8, 1, 256, F16, E4M3, 16, [130], [6], "random"), (8, 2, 128, F16, E4M3, 1024, [1500, 3], [20, 64], "random"),
     (3, 1, 128, BF16, BF16, 16, [1000, 2, 640], [2, 40, 11], "random"), (64, 8, 128, F16, F16, 16, [700], [1], "none"),
     (16, 16, 64, BF16, E4M3, 16, [40], [31], "none"),
+    # several row blocks over the same keys and values
+    (16, 1, 128, BF16, BF16, 16, [513, 77], [33, 20], "random"), (24, 2, 64, F16, F16, 16, [400], [50], "random"),
+    (8, 1, 64, F16, E4M3, 32, [300, 0], [40, 64], "random"), (7, 1, 256, BF16, E4M3, 16, [260], [30], "none"),
+    # more pieces of a row than its four waves take at once
+    (2, 1, 64, F16, F16, 256, [60000], [1], "none"),
 ]
 
 
@@ -434,6 +439,18 @@ def test_attention_of_scores_near_the_lowest_number():
         out = ubw.tree_attn(q, cache, table, i32([0, 2]), i32([0]), max_tree=2, scale=1.0, lse=lse, workspace=ws)
         assert torch.equal(out, cache.v[0, 0, 0].expand_as(out))
         assert torch.allclose(lse, torch.full_like(lse, float(q[0, 0, 0].double() * cache.k[0, 0, 0, 0].double())), rtol=1e-6)
+
+
+def test_attention_of_one_layer_of_many():
+    g = gen(19)
+    k, v = (randn((3, 5, 2, 16, 64), BF16, g) for _ in "kv")
+    cache = ubw.KVCache(k, v)
+    q, table = randn((2, 4, 64), BF16, g), i32([[4, 2, 0, 1]])
+    for layer in range(3):
+        attend_and_check(q, cache.layer(layer), table, [0, 2], [50], None)
+    # a call that takes one layer takes the first of many
+    first = ubw.tree_attn(q, cache, table, i32([0, 2]), i32([50]), max_tree=2)
+    assert torch.equal(first, ubw.tree_attn(q, cache.layer(0), table, i32([0, 2]), i32([50]), max_tree=2))
 
 
 def test_attention_cuts_what_it_cannot_use():
