@@ -591,6 +591,9 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     }
                     pf[m][n] = u32x4{pack<TQ>(pr[0], pr[1]), pack<TQ>(pr[2], pr[3]), pack<TQ>(pr[4], pr[5]), pack<TQ>(pr[6], pr[7])};
                 }
+            // This wave goes first while it feeds the matrix cores and the other wave of its SIMD computes
+            // weights: 128 rows of 8 bits 626 -> 590 us, of 16 bits 171 -> 163, few rows unchanged.
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -599,6 +602,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
 #pragma unroll
                     for (int m = 0; m < MT; ++m) o[m][e] = H::mfma(v, pf[m][n], o[m][e]);
                 }
+            __builtin_amdgcn_s_setprio(0);
         };
         uint32_t at = tile0;
         for (int tb = base; tb < t_end; tb += STEP) {
