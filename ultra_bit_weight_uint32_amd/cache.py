@@ -22,6 +22,7 @@ from . import UBW_BF16, UBW_E4M3, UBW_F16, UBW_F32, KVCacheDesc, PagePoolDesc, _
 _TYPES = {torch.float32: UBW_F32, torch.float16: UBW_F16, torch.bfloat16: UBW_BF16, torch.float8_e4m3fn: UBW_E4M3}
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -29,7 +30,7 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _launch(fn, index, *args):
     """The call of a library function on a device, on that device's current stream."""
     f = getattr(lib(), fn)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = f(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
@@ -64,9 +65,10 @@ def _rows(t, name, index, dim, heads=None, tokens=None, dtype=None):
     be apart (a part of a fused buffer)."""
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         _elsewhere(t, name, index)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {list(t.shape)}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {list(shape)}")
+    n, h, d = shape
     if d != dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
         raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, "
                          f"{'heads' if heads is None else heads}, {dim}], got {list(t.shape)}")
