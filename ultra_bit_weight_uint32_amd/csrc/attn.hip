@@ -47,6 +47,7 @@ namespace {
 using h16 = _Float16;
 using b16 = __bf16;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
@@ -58,6 +59,7 @@ struct Half<h16> {
     typedef h16 x2 __attribute__((ext_vector_type(2)));
     typedef h16 x8 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7c00;
+    static constexpr bool kSplits = false;
     static __device__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -71,6 +73,7 @@ struct Half<b16> {
     typedef b16 x2 __attribute__((ext_vector_type(2)));
     typedef b16 x8 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7f80;
+    static constexpr bool kSplits = true;
     static __device__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -270,6 +273,55 @@ __device__ inline uint32_t not_finite(uint32_t w) {
     }
 }
 
+// 128 bf16 values of a row (32 of this lane, in q[0 .. 3], the others in the row's other three lanes) as two
+// e4m3 parts each, x = 2^u hi + 2^(u - 5) lo: hi is x rounded to 4 bits, what is left of 8 bits fits lo's 4.
+// Values below 2^-13 of the row's largest are off by up to 2^-22 of it (less than the fp32 sums of a score
+// lose). q[0 .. 1] get hi, q[2 .. 3] lo; returns the parts' powers of two as biased bytes 0 and 1 (one
+// power for the row: the product applies those of its four lanes to 32 of the 128 dims each, and these are
+// not the lanes that hold them). Infinities become NaN, which scores with them end in anyway.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+constexpr int kOne8 = 0x7f;  // the power 2^0
+__device__ inline i32x8 joined(u32x4 a, u32x4 b) {
+    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+__device__ inline int split_query(u32x4* q) {
+    uint32_t top = 0;  // exponent of the largest, in place
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t w = q[i >> 2][i & 3];
+        const uint32_t a = w & 0x7f80u, b = (w >> 16) & 0x7f80u;
+        top = max(top, max(a == 0x7f80u ? 0u : a, b == 0x7f80u ? 0u : b));
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    const int e = max((int)(top >> 7), 12);
+    const float up = __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);  // 2^(134 - e): the largest comes to [128, 256)
+    u32x4 hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w[2] = {q[i >> 1][2 * (i & 1)], q[i >> 1][2 * (i & 1) + 1]};
+        int h = 0, r = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float x = __builtin_bit_cast(float, w[k] << 16), y = __builtin_bit_cast(float, w[k] & 0xffff0000u);
+            x = __builtin_isfinite(x) ? x * up : __builtin_nanf("");
+            y = __builtin_isfinite(y) ? y * up : __builtin_nanf("");
+            h = k ? __builtin_amdgcn_cvt_pk_fp8_f32(x, y, h, true) : __builtin_amdgcn_cvt_pk_fp8_f32(x, y, h, false);
+            const f32x2 z = k ? __builtin_amdgcn_cvt_pk_f32_fp8(h, true) : __builtin_amdgcn_cvt_pk_f32_fp8(h, false);
+            x = (x - z.x) * 32.f;
+            y = (y - z.y) * 32.f;
+            r = k ? __builtin_amdgcn_cvt_pk_fp8_f32(x, y, r, true) : __builtin_amdgcn_cvt_pk_fp8_f32(x, y, r, false);
+        }
+        hi[i >> 2][i & 3] = (uint32_t)h;
+        lo[i >> 2][i & 3] = (uint32_t)r;
+    }
+    q[0] = hi[0];
+    q[1] = hi[1];
+    q[2] = lo[0];
+    q[3] = lo[1];
+    return (e - 7) | (e - 12) << 8;
+}
+
 constexpr int kW = 2;
 // MT row tiles a wave, R waves side by side over rows, T over positions, NS tiles of 32 positions a
 // step, NB steps in LDS for each of the T.
@@ -307,6 +359,10 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     __shared__ __align__(1024) char buf[C::kLds];
     const uint32_t buf0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)buf;
     float* o_lds = reinterpret_cast<float*>(buf);
+
+    // bf16 queries over 8-bit keys of 128 dims or more: queries as two e4m3 parts (split_query)
+    constexpr bool kSplit = FP8 && D >= 128 && Half<TQ>::kSplits;
+    constexpr int NG = kSplit ? D / 128 : 1;
 
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -445,6 +501,12 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 q[m][ks] = r < rows ? *reinterpret_cast<const u32x4*>(at + d * 2) : u32x4{0, 0, 0, 0};
             }
         }
+        int qscale[MT][NG];
+        if constexpr (kSplit)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) qscale[m][g] = split_query(&q[m][4 * g]);
         float ks_scale = 1.f, vs_scale = 1.f;
         if constexpr (FP8) {
             if (a.c.k_scale) ks_scale = a.c.k_scale[h];
@@ -493,6 +555,21 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             for (int sub = 0; sub < 2 * NS; ++sub) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m) sc[m][sub] = less[m];
+                if constexpr (kSplit) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t from = at + (sub >> 1) * L::kBytes + ((sub & 1) * L::KL + 2 * g) * 1024 + lane * 16;
+                        const i32x8 kk = joined(*lds_at<const u32x4>(from), *lds_at<const u32x4>(from + 1024));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            sc[m][sub] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                kk, joined(q[m][4 * g], q[m][4 * g + 1]), sc[m][sub], 0, 0, 0, kOne8, 0, qscale[m][g]);
+                            sc[m][sub] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                kk, joined(q[m][4 * g + 2], q[m][4 * g + 3]), sc[m][sub], 0, 0, 0, kOne8, 1, qscale[m][g]);
+                        }
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t from = at + (sub >> 1) * L::kBytes + (sub & 1) * L::KL * 1024 + lane * 16;
