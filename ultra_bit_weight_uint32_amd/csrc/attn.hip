@@ -322,7 +322,6 @@ __device__ inline int split_query(u32x4* q) {
     return (e - 7) | (e - 12) << 8;
 }
 
-constexpr int kW = 2;
 // MT row tiles a wave, R waves side by side over rows, T over positions, NS tiles of 32 positions a
 // step, NB steps in LDS for each of the T.
 template <bool FP8, int D, int MT, int R, int T, int NS, int NB>
@@ -331,9 +330,10 @@ struct Cfg {
     static constexpr int kTiles = T * NB * NS * Layout<FP8, D>::kBytes;
     static constexpr int kJoin = (T - 1) * RB * (D + 4) * 4;  // laid over the tiles
     static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
-    // workgroups per CU: by LDS, and waves per SIMD by registers
+    // workgroups per CU: by LDS, and waves per SIMD by registers (with three waves the largest tiles spill: 64 rows of 8
+    // bits over 16K positions of 8 sequences 111 us, with two 68)
     static constexpr int kFit = (160 * 1024 - 512) / (kLds + 8 * T * RB + 1024);
-    static constexpr int kWaves = D * MT > 256 ? 1 : D * MT == 256 ? (NS == 1 ? 3 : kW) : 3;
+    static constexpr int kWaves = D * MT == 256 ? 2 : 3;
     static constexpr int kMost = kWaves * 256 / kThreads;
     static constexpr int kPerCu = kFit < kMost ? kFit : kMost;
     static constexpr int kSimd = kPerCu * kThreads / 256 < 1 ? 1 : kPerCu * kThreads / 256;
@@ -904,7 +904,8 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
 }
 
 template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>
-hipError_t launch(const AttnArgs& a, hipStream_t s) {
+hipError_t launch(const AttnArgs& a, AttnTile t, hipStream_t s) {
+    if (t.tiles != MT || t.row_waves != R) return hipErrorInvalidValue;  // the workspace is cut for this tile
     using C = Cfg<FP8, D, MT, R, T, NS, NB>;
     const int64_t rows = (int64_t)a.max_tree * a.group, pairs = (int64_t)a.batch * a.c.heads;
     const int64_t most = a.target > 0 ? a.max_items : pairs * cdiv(rows, C::RB);
@@ -924,14 +925,15 @@ template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const AttnArgs& a, AttnTile t, hipStream_t s) {
     const bool one_block = a.max_tree * a.group <= attn_rows(t);
     if constexpr (D == 256) {
-        if (t.row_waves == 1) return launch<TQ, FP8, D, 1, 1, 2, 1, 2, true>(a, s);
-        return one_block ? launch<TQ, FP8, D, 1, 4, 1, 1, 2, true>(a, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2, false>(a, s);
+        // 16 bits: 8 sequences of 16K positions with NB = 1 96 us, with 2 (one workgroup a CU) 132
+        if (t.row_waves == 1) return launch<TQ, FP8, D, 1, 1, 2, 1, FP8 ? 2 : 1, true>(a, t, s);
+        return one_block ? launch<TQ, FP8, D, 1, 4, 1, 1, 2, true>(a, t, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2, false>(a, t, s);
     } else {
         constexpr int NB = FP8 || D == 64 ? 2 : 1;
-        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1, 4, 1, NB, true>(a, s);
-        if (t.row_waves == 1) return launch<TQ, FP8, D, 2, 1, 4, 1, NB, true>(a, s);
-        if (t.row_waves == 2) return launch<TQ, FP8, D, 2, 2, 2, 1, 2, true>(a, s);
-        return one_block ? launch<TQ, FP8, D, 2, 4, 1, 2, 2, true>(a, s) : launch<TQ, FP8, D, 2, 4, 1, 2, 2, false>(a, s);
+        if (t.tiles == 1) return launch<TQ, FP8, D, 1, 1, 4, 1, NB, true>(a, t, s);
+        if (t.row_waves == 1) return launch<TQ, FP8, D, 2, 1, 4, 1, NB, true>(a, t, s);
+        if (t.row_waves == 2) return launch<TQ, FP8, D, 2, 2, 2, 1, 2, true>(a, t, s);
+        return one_block ? launch<TQ, FP8, D, 2, 4, 1, 2, 2, true>(a, t, s) : launch<TQ, FP8, D, 2, 4, 1, 2, 2, false>(a, t, s);
     }
 }
 template <typename TQ, bool FP8>
