@@ -244,16 +244,17 @@ def attend_and_check(q, cache, table, start, ctx, masks, scale=None, split=True,
     return out, lse, want
 
 
-def check_attention(out, lse, want, dtype, most):
+def check_attention(out, lse, want, dtype, most, more=0.0):
     """Against 64 bits. Scores: a sum of dim products of exact factors and a product with the scale, then
     the difference to the maximum before the exponential (which is good to 2 V): ds <= (dim + 4) V reach
     + 4 V (|s| + 16) with |s| <= reach. Weights are off by 2 ds relatively, each rounded to the type
     once (u), or by half of fp16's smallest step, 2^-25 where the largest weight is 2^7 or more. Sums
-    over `most` positions, the parts' scaling and the division: (most + 64) V. Then one rounding."""
+    over `most` positions, the parts' scaling and the division: (most + 64) V. Then one rounding. `more`:
+    what scores are off by besides."""
     ref, ref_lse, size, reach = want
     dim = ref.shape[-1]
     u = half_step(dtype)
-    ds = ((dim + 4) * V * reach + 4 * V * (reach + 16))[..., None]
+    ds = ((dim + 4) * V * reach + 4 * V * (reach + 16) + more)[..., None]
     rel = u + 2 * ds + (most + 64) * V
     # the smallest steps add at most most 2^-32 of the largest |v| < 6 (normal values, scales below 1.5)
     off = rel * size + most * 2.0 ** -32 * 9
@@ -320,6 +321,35 @@ def test_attention(case, split):
     # the same call again gives the same bits, and a stated length changes nothing but the split
     again = attend_and_check(q, cache, table, start, ctx, m, split=split, max_len=max(c + n for c, n in zip(ctx, drafts)))
     assert split or (torch.equal(out, again[0]) and torch.equal(lse, again[1]))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("tokens", [1, 4, 8, 33])
+def test_attention_of_queries_of_many_sizes(tokens, dim):
+    """bf16 queries whose elements lie far apart, over 8-bit keys. Elements may be taken to 2^-22 of the
+    row's largest: scores are off by up to 2^-22 max |q| scale sum |k| more. Among the rows are zeros, one
+    element alone, the smallest numbers, and one large element among small ones."""
+    g = gen(90 + dim + tokens)
+    ctx = [150]
+    table, pages = batch_of(ctx, [tokens], 16, g)
+    cache = cache_of(pages, 1, 16, dim, E4M3, g)
+    q = randn((tokens, 8, dim), F32, g)
+    q *= torch.exp2(torch.randint(-20, 2, q.shape, device=DEV, generator=g).float())
+    q[:, 1] = 0
+    q[:, 2, 1:] = 0
+    q[:, 3] *= 2.0 ** -100
+    q[:, 4] *= 2.0 ** -122   # to the smallest bf16 numbers and below
+    q[:, 5, dim - 1] = 3.0
+    q[:, 6, 5] = 2.0 ** 20
+    q = q.to(BF16)
+    out = torch.empty_like(q)
+    lse = torch.empty((tokens, 8), device=DEV)
+    start = [0, tokens]
+    ubw.tree_attn(q, cache, table, i32(start), i32(ctx), None, max_tree=tokens, out=out, lse=lse)
+    want = attention_reference(q, cache, table, start, ctx, None)
+    k = cache.k.float().abs().sum(-1).max().item() * (1.0 if cache.k_scale is None else cache.k_scale.max().item())
+    more = 2.0 ** -22 * dim ** -0.5 * k * q.float().abs().amax(-1).double().cpu()
+    check_attention(out, lse, want, BF16, table.shape[1] * cache.page_size, more)
 
 
 def test_attention_repeats_bit_for_bit():
