@@ -13,7 +13,9 @@
 //   * O^T = V^T P^T: those eight weights, packed to 16 bits, are the B operand as they are, if the
 //     operand's k index counts positions in that order. For A, transposing LDS reads give lane (dim, j)
 //     the same eight positions of its dim; value rows lie with their 16-byte columns exchanged by XOR so
-//     that these reads spread over the banks. 8-bit values are read so too and widened on the way.
+//     that these reads spread over the banks. 8-bit values are read so too and widened on the way; 8-bit
+//     keys are widened as well, or (bf16 queries, 128 dims or more) multiplied as they are by queries in
+//     two 8-bit parts, which costs the matrix cores the same and the vector unit nothing: 512 rows 520 -> 455 us.
 //   * m is not followed exactly: o is scaled only when a score passes m by more than 2^8 (a wave-uniform
 //     branch that long contexts take a few times), so the usual step has no cross-lane work at all, l is
 //     kept per lane, and p = 2^((s - m) log2 e + 7) stays below 2^15, inside fp16, while weights down to
@@ -33,11 +35,12 @@
 // Split over workgroups: the pieces (sequence, head, row block, run of positions) are cut on the
 // device from the lengths, of equal size, and taken by a grid of resident workgroups; a piece that is not
 // a whole sequence leaves o, m, l in the workspace and k_join adds them up in order. Few rows take about
-// three pieces a workgroup (ragged batches: 249 against 269 us), many rows one (their sums are large:
-// 170 against 198 us).
+// three pieces a workgroup where each is long enough (64 ragged sequences: 249 against 269 us), many rows
+// one (their sums are large: 170 against 198 us).
 //
-// Bound: HBM up to about 128 rows (5.0 to 5.3 TB/s of keys and values, where a plain streaming read of
-// this card reaches 6.4); beyond, the vector unit beside the matrix cores.
+// Bound: HBM up to about 64 rows (5.0 to 5.8 TB/s of keys and values over long contexts, where a plain
+// streaming read of this card reaches 6.4); beyond, the vector unit beside the matrix cores (957 TFLOP/s
+// at 512 rows of 128 dims in 8 bits); short contexts, a chain of a dozen memory latencies (10 us).
 #include "cache_internal.h"
 
 namespace ubw {
@@ -167,8 +170,11 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, bool one_row_wave, in
     const int per = (a.batch + NT - 1) / NT;
     const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
     int64_t units = 0;
+    // a thread's first sequence, most often its only one, is loaded once
+    const Seq s0 = b0 < b1 ? seq_of(a, b0) : Seq{0, 0, 0};
+    const auto seq = [&](int b) { return b == b0 ? s0 : seq_of(a, b); };
     for (int b = b0; b < b1; ++b) {
-        const Plan p = plan_of(a, seq_of(a, b), rb, 0);
+        const Plan p = plan_of(a, seq(b), rb, 0);
         units += (int64_t)p.units * p.blocks;
     }
     const int64_t total = wg_sum<NT>(units, lds) * a.c.heads;
@@ -178,7 +184,7 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, bool one_row_wave, in
     for (int step = 0;; ++step) {
         mine = 0;
         for (int b = b0; b < b1; ++b) {
-            const Plan p = plan_of(a, seq_of(a, b), rb, chunk);
+            const Plan p = plan_of(a, seq(b), rb, chunk);
             mine += p.splits * p.blocks * a.c.heads;
         }
         const int64_t pieces = wg_sum<NT>(mine, lds);
@@ -198,7 +204,7 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, bool one_row_wave, in
     int first = y - mine;
     for (int w = 0; w < (tid >> 6); ++w) first += sums[w];
     for (int b = b0; b < b1; ++b) {
-        const Plan p = plan_of(a, seq_of(a, b), rb, chunk);
+        const Plan p = plan_of(a, seq(b), rb, chunk);
         pre[b] = first;
         first += p.splits * p.blocks * a.c.heads;
     }
@@ -234,10 +240,10 @@ struct Layout {
 };
 
 // 16 bytes a lane from memory straight to LDS at `lds` + 16 lane. The compiler does not see the
-// transfer: waits are placed by hand (m0 it sets itself wherever it uses it). ONCE: nobody else reads these bytes (keys and values under one row
-// block), they need not stay in the L2 (1.3 GB in 64 ragged sequences: 229 us, 249 without; 0.85 GB under
-// one block of 128 rows 161, 169 without; under four row blocks they are read again: 638 us without, 648
-// with).
+// transfer: waits are placed by hand (m0 it sets itself wherever it uses it). ONCE: nobody else reads these
+// bytes (keys and values under one row block), they need not stay in the L2 (1.3 GB in 64 ragged sequences:
+// 229 us, 249 without; 0.85 GB under one block of 128 rows 161, 169 without; under four row blocks they are
+// read again: 638 us without, 648 with).
 template <bool ONCE>
 __device__ inline void to_lds(Rsrc r, uint32_t off, uint32_t lds) {
     if constexpr (ONCE)
