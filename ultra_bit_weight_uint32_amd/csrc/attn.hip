@@ -844,11 +844,23 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     for (int e = 0; e < N; ++e) o[e] = 0.f;
     for (int k0 = s0; k0 < p.splits; k0 += 64 * WAVES) {
         const int mine = k0 + lane * WAVES, count = min(64, (p.splits - k0 + WAVES - 1) / WAVES);
+        float y[8][N];
+        const auto request = [&](int k) {  // eight rows
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float* from = piece_rows(a, first + (k0 + min(k + i, count - 1) * WAVES) * p.blocks, rb, D) + rl * D + lane * N;
+#pragma unroll
+                for (int e = 0; e < N; ++e) y[i][e] = from[e];
+            }
+        };
+        // beside the maxima and sums, not behind them (both launches over 500 positions 13.9 -> 13.6 us, over
+        // 4000 positions of 8 trees of 16 tokens 47.6 -> 46.8)
+        request(0);
         float mk = kLow, lk = 0.f;
         if (lane < count) {
-            const float2 y = *reinterpret_cast<const float2*>(piece_rows(a, first + mine * p.blocks, rb, D) + rb * D + 2 * rl);
-            mk = y.x;
-            lk = y.y;
+            const float2 x = *reinterpret_cast<const float2*>(piece_rows(a, first + mine * p.blocks, rb, D) + rb * D + 2 * rl);
+            mk = x.x;
+            lk = x.y;
         }
         float to = mk;
 #pragma unroll
@@ -862,14 +874,8 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
         l = l * f + lk;
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] *= f;
-        for (int k = 0; k < count; k += 8) {  // eight rows requested at a time
-            float y[8][N];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float* from = piece_rows(a, first + (k0 + min(k + i, count - 1) * WAVES) * p.blocks, rb, D) + rl * D + lane * N;
-#pragma unroll
-                for (int e = 0; e < N; ++e) y[i][e] = from[e];
-            }
+        for (int k = 0; k < count; k += 8) {
+            if (k) request(k);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float w = __shfl(g, (k + i) & 63);
