@@ -510,7 +510,8 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
  *   masks      uint64 [tokens] or NULL;  lse fp32 [tokens][heads] or NULL
  *   workspace  ubw_tree_attn_workspace_bytes() bytes of scratch, or NULL with 0 bytes. With it long
  *              contexts are split over workgroups and joined by a second launch (in a fixed order:
- *              results do not vary from run to run). It needs no initialization and keeps nothing
+ *              results do not vary from run to run), short ones are not where max_len or table_cols *
+ *              page_size shows them to be short. It needs no initialization and keeps nothing
  *              between calls; calls that may run at the same time need their own.
  * Nothing in device memory is trusted for addresses: lengths, starts and table entries out of range
  * are cut as above. tokens = 0 or batch = 0 enqueues nothing.

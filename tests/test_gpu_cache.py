@@ -302,12 +302,13 @@ ATTEND = [  # heads, kv, dim, q type, cache type, page, contexts, tokens, masks
 ]
 
 
-@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("split", [True, False, "long table"])
 @pytest.mark.parametrize("case", ATTEND, ids=str)
 def test_attention(case, split):
+    """With a workspace, without one, and with a table so long that short contexts are split too."""
     heads, kv, dim, qt, ct, page, ctx, drafts, masks = case
     g = gen(heads + dim + page + sum(ctx))
-    table, pages = batch_of(ctx, drafts, page, g)
+    table, pages = batch_of(ctx, drafts, page, g, cols=1 + 1024 // page if split == "long table" else 0)
     cache = cache_of(pages, kv, page, dim, ct, g, token_major=heads % 2 == 1)
     t = sum(drafts)
     start = [0] + list(np.cumsum(drafts))

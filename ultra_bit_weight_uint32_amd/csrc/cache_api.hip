@@ -141,9 +141,9 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     a.lse = lse;
     a.ws = static_cast<float*>(workspace);
     a.max_items = attn_max_items(batch, rows, c.kv_heads, c.head_dim, t);
-    // contexts of one unit (or known to be) are not split: one launch
-    const int64_t longest = max_len > 0 ? max_len : (int64_t)table_cols * c.page_size;
-    a.target = workspace && longest > kAttnUnit ? attn_target(t, c.head_dim) : 0;
+    // short contexts (as the table or the caller says) are not split: one launch
+    const int64_t room = (int64_t)table_cols * c.page_size, longest = max_len > 0 && max_len < room ? max_len : room;
+    a.target = workspace && longest > attn_unsplit(t, c.head_dim, (int64_t)batch * c.kv_heads) ? attn_target(t, c.head_dim) : 0;
     return hip_status(launch_attn(a, c.dtype, q_dtype, c.head_dim, t, as_stream(stream)));
 }
 

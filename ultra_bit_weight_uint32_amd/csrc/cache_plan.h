@@ -102,6 +102,20 @@ inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
     return AttnTile{2, 4};
 }
 
+// Contexts of up to this many positions (with their tokens) are not split: a few more steps of one
+// workgroup take less than cutting the batch and joining its pieces in a second launch. By the positions
+// a workgroup takes in one step: 128 with one row wave (64 dims and 128), of 256 dims 64; two row waves
+// 64, four 64 and of 256 dims 32. 128 dims of 16 bits, split and not, for one sequence and for eight:
+// 8 rows at 500 positions 13.6 and 11.2 us, 15.2 and 12.7, at 760 13.8 and 13.5, 18.2 and 16.2, at 1000
+// 13.7 and 15.7, 18.3 and 19.9; 64 rows at 380 16.9 and 17.2, 21.8 and 18.1, at 760 16.7 and 23.1, 28.5 and
+// 24.8; 128 rows at 200 18.7 and 16.2, 25.1 and 16.5, at 380 19.4 and 22.6, 28.9 and 22.9. 256 dims, 8 rows
+// at 200 17.5 and 16.2, at 380 17.6 and 20.6. So many rows of 64 and more (sequence, key/value head) pairs,
+// which use a quarter of the card as they are, have twice the limit.
+inline int attn_unsplit(AttnTile t, int head_dim, int64_t pairs) {
+    if (head_dim == 256) return t.row_waves == 1 ? 256 : 128;
+    return t.row_waves == 1 ? 768 : (t.row_waves == 2 ? 384 : 256) * (pairs >= 64 ? 2 : 1);
+}
+
 // How a batch is cut: sequence b has blocks_b row blocks of units_b units of positions for each
 // key/value head; a piece is one block over `chunk` units at most, a sequence's pieces of equal size
 // but for one unit. chunk starts at total / target and grows while there are more pieces than that.
