@@ -39,7 +39,7 @@
 // one (their sums are large: 170 against 198 us).
 //
 // Bound: HBM up to about 64 rows (5.0 to 5.8 TB/s of keys and values over long contexts, where a plain
-// streaming read of this card reaches 6.4); beyond, the vector unit beside the matrix cores (957 TFLOP/s
+// streaming read of this card reaches 6.4); beyond, the vector unit beside the matrix cores (1.0 PFLOP/s
 // at 512 rows of 128 dims in 8 bits); short contexts, a chain of a dozen memory latencies (10 us).
 #include "cache_internal.h"
 
