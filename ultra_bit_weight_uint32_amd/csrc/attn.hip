@@ -582,7 +582,8 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         };
         const auto scores = [&](uint32_t at, f32x4 (&sc)[MT][2 * NS]) {
             // read ahead of the products, as the values below (512 rows of 8 bits, fp16 queries 253 -> 235 us with both)
-            constexpr int AHEAD = kSplit ? 2 : 4;
+            constexpr int AHEAD = kSplit || NK < 4 ? 2 : 4;
+            static_assert(AHEAD <= NK, "reads stay inside the step");
             Keys raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) raw[i] = keys(at, i);
@@ -692,6 +693,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             // products ahead (left to itself the compiler waits for every read behind its request: four 64-token
             // trees over 12K positions of 256 dims in 8 bits 317 us, 258 so; of 128 dims 238 and 231).
             constexpr int AHEAD = 4, NV = NS * NE;
+            static_assert(AHEAD <= NV, "reads stay inside the step");
             Values raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) raw[i] = turned(at + i / NE * L::kBytes, i % NE);
