@@ -22,6 +22,8 @@ from . import UBW_BF16, UBW_E4M3, UBW_F16, UBW_F32, KVCacheDesc, PagePoolDesc, _
 _TYPES = {torch.float32: UBW_F32, torch.float16: UBW_F16, torch.bfloat16: UBW_BF16, torch.float8_e4m3fn: UBW_E4M3}
 
 
+_Tensor = torch.Tensor
+_calls = {}   # library functions by name
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -29,7 +31,9 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _launch(fn, index, *args):
     """The call of a library function on a device, on that device's current stream."""
-    f = getattr(lib(), fn)
+    f = _calls.get(fn)
+    if f is None:
+        f = _calls[fn] = getattr(lib(), fn)
     if _current_device() == index:
         st = f(*args, _current_stream(index))
     else:
@@ -46,7 +50,11 @@ def _elsewhere(t, name, index):
 
 
 def _flat(t, name, dtype, index, numel=None, shape=None):
-    """Pointer of a contiguous tensor of a dtype on the call's device."""
+    """Pointer of a contiguous tensor of a dtype on the call's device. (All conditions at once first: a
+    single-token call spends half its time in these questions.)"""
+    if type(t) is _Tensor and t.get_device() == index and t.dtype is dtype and (numel is None or t.numel() == numel) and \
+            t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         _elsewhere(t, name, index)
     if t.dtype is not dtype:
@@ -63,12 +71,12 @@ def _flat(t, name, dtype, index, numel=None, shape=None):
 def _rows(t, name, index, dim, heads=None, tokens=None, dtype=None):
     """(pointer, row stride, tokens, heads) of [tokens, heads, dim] whose heads are contiguous; rows may
     be apart (a part of a fused buffer)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+    if not isinstance(t, _Tensor) or t.get_device() != index:
         _elsewhere(t, name, index)
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {list(shape)}")
-    n, h, d = shape
+    try:
+        n, h, d = t.shape
+    except ValueError:
+        raise ValueError(f"{name} must be [tokens, heads, {dim}], got {list(t.shape)}") from None
     if d != dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
         raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, "
                          f"{'heads' if heads is None else heads}, {dim}], got {list(t.shape)}")
