@@ -360,9 +360,10 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     extern __shared__ int pre[];  // [batch + 1], with a split
     __shared__ int64_t lds64[4];
     __shared__ float ml[T][RB][2];
-    __shared__ int odd[2];  // of this piece and the next: values of the tree that are not finite were met
-    if (threadIdx.x == 0) odd[0] = 0;
-    int turn = 0;
+    // Of each wave: it met values of the tree that are not finite in this piece. A wave clears and sets its own
+    // word only, so both come in its own order; the others read it behind a barrier of the piece's end, and
+    // the piece's last barrier stands before the next clearing.
+    __shared__ int odd[R * T];
     __shared__ __align__(1024) char buf[C::kLds];
     const uint32_t buf0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)buf;
     float* o_lds = reinterpret_cast<float*>(buf);
@@ -409,7 +410,6 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         int b, h, blk, split;
         Seq s;
         Plan p;
-        if (threadIdx.x == 0) odd[turn ^ 1] = 0;
         if (a.target > 0) {
             int lo = 0, hi = a.batch;  // the last b with pre[b] <= item
             while (hi - lo > 1) {
@@ -434,6 +434,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             split = 0;
             if (blk >= p.blocks) continue;
         }
+        if (lane == 0) odd[wave] = 0;
         const int rows = s.n * a.group, len = positions(a, s);
         int u0, u1;
         attn_range(p.units, p.splits, split, &u0, &u1);
@@ -646,7 +647,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     *w = y & ~nf;
                 }
             }
-            if (found) odd[turn] = 1;
+            if (found) odd[wave] = 1;
         };
         // A tile at LDS address `at`.
         const auto step = [&](uint32_t at, bool whole) {
@@ -813,7 +814,10 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
 #pragma unroll
                     for (int e = 0; e < NE; ++e) o[m][e] += *reinterpret_cast<const f32x4*>(o_lds + (w * RB + rl) * kRow + 16 * e + 4 * j);
                 const int t = r / a.group, hq = h * a.group + (r - t * a.group);
-                if (odd[turn]) {  // what clean() took out: infinite or NaN for the rows that see it
+                int odds = 0;
+#pragma unroll
+                for (int w = 0; w < R * T; ++w) odds |= odd[w];
+                if (odds) {  // what clean() took out: infinite or NaN for the rows that see it
                     const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
                     for (int x = max(s.ctx, u0 * U); x < t_end; ++x) {
                         const int page = page_at(x);
@@ -853,8 +857,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (mx[m] + __builtin_amdgcn_logf(l[m])) * kLn2 : -INFINITY;
             }
         }
-        __syncthreads();  // the tiles, ml and o_lds are written again by the next piece
-        turn ^= 1;
+        __syncthreads();  // the tiles, ml, odd and o_lds are written again by the next piece
     }
 }
 
