@@ -72,3 +72,81 @@ def test_tree_values_that_are_not_finite(tokens, heads, dtype, dim, split):
             assert torch.equal(got[1], clean[1])
         for (p, r), x in zip(at, was):
             cache.v[p, 0, r, 7] = x
+
+
+# ---------------------------------------------------------------------------------------------
+# large scores
+
+APART = [(100, 101), (101, 100), (100, 132), (132, 100), (40, 700), (700, 40), (3, 1290), (1290, 3)]
+
+
+def score_cache(dtype, dim, scores, g):
+    """A one-head cache and a query row such that position p's score (scale 1) is exactly scores[p]: whole
+    numbers below 2^11 in one dim, where the query has 1, and multiples of 2^27 over 16 dims of 2^15 x 2^8."""
+    page, n = 16, len(scores)
+    table, pages = batch_of([n - 1], [1], page, g, cols=columns(page, True))
+    cache = cache_of(pages, 1, page, dim, dtype, g, scales=False)
+    q = torch.zeros(dim, device=DEV)
+    q[:16], q[20] = 2.0 ** 15, 8.0
+    k = torch.zeros((n, dim), device=DEV)
+    for p, x in enumerate(scores):
+        k[p, :16] = 256.0 * round(x / 2 ** 27)
+        k[p, 20] = (x - 2 ** 27 * round(x / 2 ** 27)) / 8
+    assert torch.equal(k.to(dtype).float(), k)
+    at = torch.arange(n, device=DEV)
+    cache.k[table[0, at // page].long(), 0, at % page] = k.to(dtype)
+    v = cache.v[table[0, at // page].long(), 0, at % page].double().cpu()
+    return cache, table, q, v
+
+
+@pytest.mark.parametrize("heads", [1, 20, 40, 100])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3], ids=str)
+def test_large_scores_weigh_by_their_difference(dtype, dim, heads):
+    """Scores of 2^27 and 2^27 - 8, both exact in fp32, at positions of one tile, of two waves and of two
+    pieces: they weigh 1 : e^-8, wherever they lie. The scores are exact, so an output is off by the
+    weights' roundings (half a step of the type; e^-8 itself by under 2^-19), those of the sums and
+    divisions (under 64 of fp32), and its own rounding."""
+    qt = BF16 if dtype is E4M3 else dtype
+    u = torch.finfo(qt).eps / 2
+    g = gen(dim + heads)
+    for hi, lo in APART:
+        scores = [0] * (max(hi, lo) + 4)
+        scores[hi], scores[lo] = 2 ** 27, 2 ** 27 - 8
+        cache, table, q, v = score_cache(dtype, dim, scores, g)
+        q = q.to(qt).expand(1, heads, dim).contiguous()
+        w = math.exp(-8)
+        want, size = (v[hi] + w * v[lo]) / (1 + w), (v[hi].abs() + w * v[lo].abs()) / (1 + w)
+        off = (u + 2.0 ** -18 + 64 * 2.0 ** -24) * size
+        tol = off + u * (want.abs() + off)
+        for split in (True, False):
+            out, lse = attend(q, cache, table, [0, 1], [len(scores) - 1], scale=1.0, split=split)
+            err = (out[0].double().cpu() - want).abs() / tol
+            assert (err <= 1).all(), (hi, lo, split, float(err.max()))
+            assert ((lse - (2 ** 27 + math.log1p(w))).abs() <= 16).all()   # one step of fp32 there
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scores_next_to_the_largest_numbers(dim):
+    """bf16 scores of 1.75 2^127 and 1.5 2^127, of either sign (times log2 e they pass fp32's range): the
+    higher one takes all, wherever the two lie, and is the log-sum-exp."""
+    g = gen(dim)
+    page = 16
+    for first, second in APART:
+        n = max(first, second) + 4
+        table, pages = batch_of([n - 1], [1], page, g, cols=columns(page, True))
+        cache = cache_of(pages, 1, page, dim, BF16, g)
+        at = torch.arange(n, device=DEV)
+        where = (table[0, at // page].long(), 0, at % page)
+        v = cache.v[where]
+        for sign in (1, -1):
+            k = torch.zeros((n, dim), device=DEV)
+            k[:, 1] = 0.0 if sign > 0 else -1.75 * 2.0 ** 63   # the others are far below
+            k[first, 1], k[second, 1] = (1.75 * 2.0 ** 63, 1.5 * 2.0 ** 63) if sign > 0 else (-1.5 * 2.0 ** 63, -1.75 * 2.0 ** 63)
+            cache.k[where] = k.to(BF16)
+            q = torch.zeros((1, 3, dim), dtype=BF16, device=DEV)
+            q[..., 1] = 2.0 ** 64
+            for split in (True, False):
+                out, lse = attend(q, cache, table, [0, 1], [n - 1], scale=1.0, split=split)
+                assert torch.equal(out, v[first].expand_as(out)), (first, second, sign, split)
+                assert (lse == sign * (1.75 if sign > 0 else 1.5) * 2.0 ** 127).all()

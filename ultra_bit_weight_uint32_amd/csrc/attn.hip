@@ -22,6 +22,7 @@
 //     2^-21 of the largest are normal fp16 numbers. m is kept as a score and -m is what the product K Q^T
 //     starts from, so that s - m costs nothing and is right at any size of s (s log2 e - m in one fused
 //     step, m rounded, is off by the rounding of m: at |s| = 10^8 the largest weight would be 2^(7 +- 4)).
+//     Waves and pieces are joined by differences of these maxima too.
 // Descriptors cover 16 rows; one of size 0 stands for rows that are not needed or on no valid page, so
 // every step issues the same transfers, their count is waited for exactly, and no table entry is ever
 // trusted. Few rows (R = 1): each wave has tiles of its own and no barrier; with one tile, its keys make
@@ -85,6 +86,11 @@ struct Half<b16> {
                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false));
     }
 };
+// What sums under the maximum m (a score; -INFINITY: of nothing) are multiplied by under the maximum `to`: a
+// difference of scores first, so that it is as exact for large scores as for small ones.
+__device__ inline float weight(float m, float to, float cc) {
+    return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - to) * cc);
+}
 template <typename T>
 __device__ inline uint32_t pack(float a, float b) {  // rounded to nearest even
     typename Half<T>::x2 v;
@@ -94,7 +100,7 @@ __device__ inline uint32_t pack(float a, float b) {  // rounded to nearest even
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLow = -3.402823466e38f;  // m of a row that has seen nothing
+constexpr float kLow = -3.402823466e38f;  // lim of a row that has seen nothing
 constexpr float kShift = 7.f, kSlack = 8.f;
 constexpr int kCus = 256;
 constexpr int kNoLds = 0xf;  // a scheduling barrier for all but arithmetic
@@ -765,10 +771,10 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         }
         wait_loads<0>();  // what was fetched beyond the end
 
-        // From here on the maximum in units of log2, with the shift: weights are 2^(s log2 e - mx).
+        // The maximum, for joining: -INFINITY where nothing was seen.
         float mx[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) mx[m] = lim[m] == kLow ? kLow : fmaxf(fmaf(ms[m], cc, -kShift), kLow);
+        for (int m = 0; m < MT; ++m) mx[m] = lim[m] == kLow ? -INFINITY : ms[m];
 
         // Join the T waves of each row over positions: every one brings its rows to the common maximum, the
         // first adds up. Lane (c, j) has row c, dims 16 e + 4 j .. + 3.
@@ -788,12 +794,12 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int r = (rw * MT + m) * 16 + c;
-                float top = kLow, sum = 0.f;
+                float top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < T; ++w) top = fmaxf(top, ml[w][r][0]);
 #pragma unroll
-                for (int w = 0; w < T; ++w) sum += ml[w][r][1] * __builtin_amdgcn_exp2f(ml[w][r][0] - top);
-                const float f = __builtin_amdgcn_exp2f(mx[m] - top);
+                for (int w = 0; w < T; ++w) sum += ml[w][r][1] * weight(ml[w][r][0], top, cc);
+                const float f = weight(mx[m], top, cc);
                 mx[m] = top;
                 l[m] = sum;
 #pragma unroll
@@ -854,7 +860,8 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     *reinterpret_cast<u32x2*>(out + 16 * e) = u32x2{pack<TQ>(o[m][e][0] * inv, o[m][e][1] * inv),
                                                                     pack<TQ>(o[m][e][2] * inv, o[m][e][3] * inv)};
                 if (a.lse && j == 0)
-                    a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (mx[m] + __builtin_amdgcn_logf(l[m])) * kLn2 : -INFINITY;
+                    a.lse[(int64_t)(s.q0 + t) * a.heads + hq] =
+                        any ? fmaf(mx[m], a.scale * ks_scale, (__builtin_amdgcn_logf(l[m]) - kShift) * kLn2) : -INFINITY;
             }
         }
         __syncthreads();  // the tiles, ml, odd and o_lds are written again by the next piece
@@ -879,7 +886,8 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     const int blk = r / rb, rl = r - blk * rb;
     const int first = before + h * p.splits * p.blocks + blk;
     const int s0 = WAVES == 4 ? wave : 0;
-    float m = kLow, l = 0.f, o[N];
+    const float scale = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.f), cc = scale * kLog2e;
+    float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = 0.f;
     for (int k0 = s0; k0 < p.splits; k0 += 64 * WAVES) {
@@ -896,7 +904,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
         // beside the maxima and sums, not behind them (both launches over 500 positions 13.9 -> 13.6 us, over
         // 4000 positions of 8 trees of 16 tokens 47.6 -> 46.8)
         request(0);
-        float mk = kLow, lk = 0.f;
+        float mk = -INFINITY, lk = 0.f;
         if (lane < count) {
             const float2 x = *reinterpret_cast<const float2*>(piece_rows(a, first + mine * p.blocks, rb, D) + rb * D + 2 * rl);
             mk = x.x;
@@ -906,7 +914,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
 #pragma unroll
         for (int d = 32; d; d >>= 1) to = fmaxf(to, __shfl_xor(to, d));
         to = fmaxf(to, m);
-        const float f = __builtin_amdgcn_exp2f(m - to), g = __builtin_amdgcn_exp2f(mk - to);
+        const float f = weight(m, to, cc), g = weight(mk, to, cc);
         lk *= g;
 #pragma unroll
         for (int d = 32; d; d >>= 1) lk += __shfl_xor(lk, d);
@@ -933,14 +941,14 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
         }
         __syncthreads();
         if (wave != 0) return;
-        float top = kLow;
+        float top = -INFINITY;
         for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
         l = 0.f;
         m = top;
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] = 0.f;
         for (int w = 0; w < 4; ++w) {
-            const float f = __builtin_amdgcn_exp2f(part[w][D] - top);
+            const float f = weight(part[w][D], top, cc);
             l += part[w][D + 1] * f;
 #pragma unroll
             for (int e = 0; e < N; ++e) o[e] = fmaf(part[w][lane * N + e], f, o[e]);
@@ -952,7 +960,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + lane * N;
 #pragma unroll
     for (int e = 0; e < N; ++e) out[e] = (TQ)(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (a.lse && lane == 0) a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? fmaf(m, scale, (__builtin_amdgcn_logf(l) - kShift) * kLn2) : -INFINITY;
 }
 
 template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>
