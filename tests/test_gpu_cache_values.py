@@ -9,7 +9,7 @@ import math
 import pytest
 
 import ultra_bit_weight_uint32_amd as ubw
-from test_gpu_cache import BF16, DEV, E4M3, F16, batch_of, cache_of, gen, i32, randn
+from test_gpu_cache import BF16, DEV, E4M3, F16, attention_reference, batch_of, cache_of, gen, i32, randn
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -150,3 +150,81 @@ def test_scores_next_to_the_largest_numbers(dim):
                 out, lse = attend(q, cache, table, [0, 1], [n - 1], scale=1.0, split=split)
                 assert torch.equal(out, v[first].expand_as(out)), (first, second, sign, split)
                 assert (lse == sign * (1.75 if sign > 0 else 1.5) * 2.0 ** 127).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# large values
+
+def check_relative(out, lse, want, most):
+    """check_attention without the steps of fp16: weights of bf16 are right to half a step (u) of
+    themselves, whatever their size, so an output is off by u + 2 ds + (most + 64) V of sum w |v| and by its
+    own rounding; ds as there."""
+    ref, ref_lse, size, reach = want
+    u, v, dim = 2.0 ** -8, 2.0 ** -24, ref.shape[-1]
+    ds = ((dim + 4) * v * reach + 4 * v * (reach + 16))[..., None]
+    off = (u + 2 * ds + (most + 64) * v) * size
+    tol = off + u * (ref.abs() + off)
+    err = (out.double().cpu() - ref).abs() / tol
+    assert (err <= 1).all(), float(err.max())
+    lerr = (lse.double().cpu() - ref_lse).abs() / (ds[..., 0] + (most + 64) * v + 4 * v * (ref_lse.abs() + 16))
+    assert (lerr <= 1).all(), float(lerr.max())
+
+
+@pytest.mark.parametrize("kind", ["largest", "signs", "lengths", "rising", "small"])
+@pytest.mark.parametrize("heads", [1, 20, 40, 100])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_bf16_values_of_every_size(dim, heads, kind):
+    """Values up to the largest bf16 numbers (their sums pass fp32 before the division), alone, in all
+    positions with one sign and with random ones, with lengths of 2^-40 to 2^127 in one row, behind scores
+    that rise (what was summed before shrinks to nothing), and values as small as 2^-100. Contexts of one
+    piece and of several, one step and many."""
+    g = gen(dim + heads)
+    page, top = 16, torch.finfo(BF16).max
+    ctx, drafts = [0, 9, 130, 1300], [1, 2, 1, 1]
+    start = [0, 1, 3, 4, 5]
+    for split in (True, False):
+        table, pages = batch_of(ctx, drafts, page, g, cols=columns(page, split))
+        cache = cache_of(pages, 1, page, dim, BF16, g)
+        v = cache.v
+        if kind == "largest":
+            v.fill_(top)
+        elif kind == "signs":
+            v.copy_(torch.where(v < 0, -top, top))
+        elif kind == "lengths":
+            v.copy_((v.float().sign() * torch.exp2(torch.randint(-40, 128, v.shape, device=DEV, generator=g).float())).to(BF16))
+        elif kind == "small":
+            v.mul_(2.0 ** -100)
+        else:
+            v.fill_(top)
+            for b, (c, n) in enumerate(zip(ctx, drafts)):
+                for p in range(c + n):
+                    at = (table[b, p // page].long(), 0, p % page)
+                    cache.k[at] = 0.0
+                    cache.k[at][0] = 128.0 if p == c + n - 1 else float(p % 50)
+                cache.v[at] = 1.0
+        q = randn((5, heads, dim), BF16, g)
+        if kind == "rising":
+            q.zero_()
+            q[..., 0] = 4.0
+        out, lse = attend(q, cache, table, start, ctx, None, split=split)
+        assert torch.isfinite(out).all()
+        check_relative(out, lse, attention_reference(q, cache, table, start, ctx, None), 1400)
+
+
+@pytest.mark.parametrize("heads", [3, 40, 100])
+def test_bf16_context_values_that_are_not_finite(heads):
+    """An infinity or NaN in the context reaches its own dim of all rows, and nothing else."""
+    g = gen(heads)
+    page, dim, ctx = 16, 128, [70, 1300]
+    for split in (True, False):
+        table, pages = batch_of(ctx, [1, 1], page, g, cols=columns(page, split))
+        cache = cache_of(pages, 1, page, dim, BF16, g)
+        q = randn((2, heads, dim), BF16, g)
+        want = attention_reference(q, cache, table, [0, 1, 2], ctx, None)
+        for p, d, x in ((3, 5, math.inf), (40, 77, -math.inf), (60, 100, math.nan)):
+            for b in range(2):
+                cache.v[table[b, p // page].long(), 0, p % page, d] = x
+        out, lse = attend(q, cache, table, [0, 1, 2], ctx, None, split=split)
+        assert (out[..., 5] == math.inf).all() and (out[..., 77] == -math.inf).all() and out[..., 100].isnan().all()
+        out[..., [5, 77, 100]] = want[0][..., [5, 77, 100]].to(DEV).to(BF16)
+        check_relative(out, lse, want, 1400)

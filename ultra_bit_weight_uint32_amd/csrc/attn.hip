@@ -18,11 +18,12 @@
 //     two 8-bit parts, which costs the matrix cores the same and the vector unit nothing: 512 rows 520 -> 455 us.
 //   * m is not followed exactly: o is scaled only when a score passes m by more than 2^8 (a wave-uniform
 //     branch that long contexts take a few times), so the usual step has no cross-lane work at all, l is
-//     kept per lane, and p = 2^((s - m) log2 e + 7) stays below 2^15, inside fp16, while weights down to
-//     2^-21 of the largest are normal fp16 numbers. m is kept as a score and -m is what the product K Q^T
+//     kept per lane, and fp16 weights p = 2^((s - m) log2 e + 7) stay below 2^15, inside fp16, while those down
+//     to 2^-21 of the largest are normal numbers (bf16 ones have fp32's range and no shift). m is kept as a score and -m is what the product K Q^T
 //     starts from, so that s - m costs nothing and is right at any size of s (s log2 e - m in one fused
 //     step, m rounded, is off by the rounding of m: at |s| = 10^8 the largest weight would be 2^(7 +- 4)).
-//     Waves and pieces are joined by differences of these maxima too.
+//     Waves and pieces are joined by differences of these maxima too, and as means of values, which never pass
+//     the largest value.
 // Descriptors cover 16 rows; one of size 0 stands for rows that are not needed or on no valid page, so
 // every step issues the same transfers, their count is waited for exactly, and no table entry is ever
 // trusted. Few rows (R = 1): each wave has tiles of its own and no barrier; with one tile, its keys make
@@ -35,7 +36,7 @@
 //
 // Split over workgroups: the pieces (sequence, head, row block, run of positions) are cut on the
 // device from the lengths, of equal size, and taken by a grid of resident workgroups; a piece that is not
-// a whole sequence leaves o, m, l in the workspace and k_join adds them up in order. Few rows take about
+// a whole sequence leaves o / l, m, l in the workspace and k_join weighs them in order. Few rows take about
 // three pieces a workgroup where each is long enough (64 ragged sequences: 249 against 269 us), many rows
 // one (their sums are large: 170 against 198 us).
 //
@@ -64,6 +65,7 @@ struct Half<h16> {
     typedef h16 x8 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7c00;
     static constexpr bool kSplits = false;
+    static constexpr float kShift = 7.f;  // of weights: see above
     static __device__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -78,6 +80,7 @@ struct Half<b16> {
     typedef b16 x8 __attribute__((ext_vector_type(8)));
     static constexpr uint32_t kExp = 0x7f80;
     static constexpr bool kSplits = true;
+    static constexpr float kShift = 0.f;
     static __device__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(x8, a), __builtin_bit_cast(x8, b), c, 0, 0, 0);
     }
@@ -101,7 +104,7 @@ __device__ inline uint32_t pack(float a, float b) {  // rounded to nearest even
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.402823466e38f;  // lim of a row that has seen nothing
-constexpr float kShift = 7.f, kSlack = 8.f;
+constexpr float kSlack = 8.f;
 constexpr int kCus = 256;
 constexpr int kNoLds = 0xf;  // a scheduling barrier for all but arithmetic
 // Words that no kernel running beside this one writes, read by the scalar unit. (As vector loads they
@@ -220,7 +223,7 @@ __device__ inline int cut_batch(const AttnArgs& a, int rb, bool one_row_wave, in
     return chunk;
 }
 
-// Workspace: pieces' rows of D sums, then (m, l) of each row.
+// Workspace: pieces' rows of D means, then (m, l) of each row.
 __device__ inline float* piece_rows(const AttnArgs& a, int item, int rb, int d) { return a.ws + (int64_t)item * rb * (d + 2); }
 
 __device__ inline Rsrc rows16(const char* p, uint32_t bytes) {
@@ -377,6 +380,16 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     // bf16 queries over 8-bit keys of 128 dims or more: queries as two e4m3 parts (split_query)
     constexpr bool kSplit = FP8 && D >= 128 && Half<TQ>::kSplits;
     constexpr int NG = kSplit ? D / 128 : 1;
+
+    // bf16 values reach as far as the fp32 sums do. A piece whose sums did not stay finite is gone through once
+    // more, with the maxima that it ended at and weights so much smaller that the sums do (unless a value is
+    // not finite itself). To look costs a piece 0.2 to 0.3 us (one token over 37 positions 7.2 -> 7.5 us, 24 ragged
+    // trees of 64 dims 25.6 -> 26.6, 64 ragged single tokens 234); values scaled down beforehand would cost
+    // the loop more, and smaller weights at once the smallest ones.
+    constexpr bool kWide = !FP8 && H::kExp == Half<b16>::kExp;
+    __shared__ int beyond[kWide ? R * T : 1];  // of each wave
+    bool again = false;
+    float ms[MT], lim[MT], shift = H::kShift;
 
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -538,13 +551,16 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         }
 
         f32x4 o[MT][NE];
-        float ms[MT], lim[MT], l[MT];
+        float l[MT];
         f32x4 less[MT];  // -ms
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            ms[m] = l[m] = 0.f;
-            lim[m] = kLow;
-            less[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (!kWide || !again) {
+                ms[m] = 0.f;
+                lim[m] = kLow;
+            }
+            l[m] = 0.f;
+            less[m] = f32x4{-ms[m], -ms[m], -ms[m], -ms[m]};
 #pragma unroll
             for (int e = 0; e < NE; ++e) o[m][e] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
@@ -713,7 +729,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                     float pr[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        pr[k] = __builtin_amdgcn_exp2f(fmaf(sc[m][2 * n + (k >> 2)][k & 3], cc, kShift));
+                        pr[k] = __builtin_amdgcn_exp2f(fmaf(sc[m][2 * n + (k >> 2)][k & 3], cc, kWide ? shift : H::kShift));
                         l[m] += pr[k];
                     }
                     pf[m][n] = u32x4{pack<TQ>(pr[0], pr[1]), pack<TQ>(pr[2], pr[3]), pack<TQ>(pr[4], pr[5]), pack<TQ>(pr[6], pr[7])};
@@ -771,46 +787,86 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         }
         wait_loads<0>();  // what was fetched beyond the end
 
-        // The maximum, for joining: -INFINITY where nothing was seen.
-        float mx[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) mx[m] = lim[m] == kLow ? -INFINITY : ms[m];
-
-        // Join the T waves of each row over positions: every one brings its rows to the common maximum, the
-        // first adds up. Lane (c, j) has row c, dims 16 e + 4 j .. + 3.
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             l[m] += __shfl_xor(l[m], 16);
             l[m] += __shfl_xor(l[m], 32);
         }
-        if constexpr (T > 1) {
+        // l becomes the sum of 2^((s - mx) log2 e). mx: -INFINITY where nothing was seen.
+        float mx[MT];
+        const int up = -(int)(kWide ? shift : H::kShift);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            mx[m] = lim[m] == kLow ? -INFINITY : ms[m];
+            l[m] = ldexpf(l[m], up);
+            if (T > 1 && j == 0) {
+                ml[tw][(rw * MT + m) * 16 + c][0] = mx[m];
+                ml[tw][(rw * MT + m) * 16 + c][1] = l[m];
+            }
+        }
+        if (kWide && !again) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};  // NaN where a sum is not finite
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-                if (j == 0) {
-                    ml[tw][(rw * MT + m) * 16 + c][0] = mx[m];
-                    ml[tw][(rw * MT + m) * 16 + c][1] = l[m];
-                }
-            __syncthreads();  // all tiles are read, all transfers done
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = (rw * MT + m) * 16 + c;
+                for (int e = 0; e < NE; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = fmaf(o[m][e][i], 0.f, x[i]);
+            const float y = (x[0] + x[1]) + (x[2] + x[3]);
+            const bool found = __any(y != y);
+            if (lane == 0) beyond[wave] = found;
+        }
+        if (T > 1 || (kWide && !again)) __syncthreads();  // all tiles are read, all transfers done
+        if constexpr (kWide) {
+            int any = 0;
+#pragma unroll
+            for (int w = 0; w < R * T; ++w) any |= beyond[w];
+            if (any && !again) {
+                int e = 1;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) e = max(e, __builtin_amdgcn_frexp_expf(l[m]));
+                shift = (float)(-1 - e);  // l 2^shift < 1/2: sums stay below half of the largest value
+                again = true;
+                it -= (int)gridDim.x;
+                continue;
+            }
+            again = false;
+            shift = H::kShift;
+        }
+
+        // The T waves of each row are brought to the common maximum, the first adds them up, weighted so that all
+        // weights' sum is 1 (fold; one wave does that at the store). Lane (c, j) has row c, dims 16 e + 4 j .. + 3.
+        float fold[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = (rw * MT + m) * 16 + c;
+            float f = 1.f;
+            if constexpr (T > 1) {
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < T; ++w) top = fmaxf(top, ml[w][r][0]);
 #pragma unroll
                 for (int w = 0; w < T; ++w) sum += ml[w][r][1] * weight(ml[w][r][0], top, cc);
-                const float f = weight(mx[m], top, cc);
+                f = weight(mx[m], top, cc);
                 mx[m] = top;
                 l[m] = sum;
+            }
+            fold[m] = l[m] > 0.f || l[m] != l[m] ? ldexpf(f, up) / l[m] : 0.f;
+            if constexpr (T > 1) {
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    o[m][e] *= f;
+                    o[m][e] *= fold[m];
                     if (tw > 0) *reinterpret_cast<f32x4*>(o_lds + ((tw - 1) * RB + r) * kRow + 16 * e + 4 * j) = o[m][e];
                 }
+                fold[m] = 1.f;
             }
-            __syncthreads();
         }
+        if constexpr (T > 1) __syncthreads();
         if (tw == 0) {
+            int odds = 0;
+#pragma unroll
+            for (int w = 0; w < R * T; ++w) odds |= odd[w];
+            odds = __builtin_amdgcn_readfirstlane(odds);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const int rl = (rw * MT + m) * 16 + c, r = blk * RB + rl;
@@ -820,9 +876,6 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
 #pragma unroll
                     for (int e = 0; e < NE; ++e) o[m][e] += *reinterpret_cast<const f32x4*>(o_lds + (w * RB + rl) * kRow + 16 * e + 4 * j);
                 const int t = r / a.group, hq = h * a.group + (r - t * a.group);
-                int odds = 0;
-#pragma unroll
-                for (int w = 0; w < R * T; ++w) odds |= odd[w];
                 if (odds) {  // what clean() took out: infinite or NaN for the rows that see it
                     const uint64_t mask = a.masks ? a.masks[s.q0 + t] : (2ull << t) - 1;
                     for (int x = max(s.ctx, u0 * U); x < t_end; ++x) {
@@ -845,23 +898,22 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 if (p.splits > 1) {
                     float* to = piece_rows(a, item, RB, D);
 #pragma unroll
-                    for (int e = 0; e < NE; ++e) *reinterpret_cast<f32x4*>(to + rl * D + 16 * e + 4 * j) = o[m][e];
+                    for (int e = 0; e < NE; ++e) *reinterpret_cast<f32x4*>(to + rl * D + 16 * e + 4 * j) = o[m][e] * fold[m];
                     if (j == 0) {
                         to[RB * D + 2 * rl] = mx[m];
                         to[RB * D + 2 * rl + 1] = l[m];
                     }
                     continue;
                 }
-                const bool any = l[m] > 0.f || l[m] != l[m];
-                const float inv = any ? vs_scale / l[m] : 0.f;
                 TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + 4 * j;
+                const float f = fold[m] * vs_scale;
 #pragma unroll
                 for (int e = 0; e < NE; ++e)
-                    *reinterpret_cast<u32x2*>(out + 16 * e) = u32x2{pack<TQ>(o[m][e][0] * inv, o[m][e][1] * inv),
-                                                                    pack<TQ>(o[m][e][2] * inv, o[m][e][3] * inv)};
+                    *reinterpret_cast<u32x2*>(out + 16 * e) =
+                        u32x2{pack<TQ>(o[m][e][0] * f, o[m][e][1] * f), pack<TQ>(o[m][e][2] * f, o[m][e][3] * f)};
                 if (a.lse && j == 0)
                     a.lse[(int64_t)(s.q0 + t) * a.heads + hq] =
-                        any ? fmaf(mx[m], a.scale * ks_scale, (__builtin_amdgcn_logf(l[m]) - kShift) * kLn2) : -INFINITY;
+                        l[m] == 0.f ? -INFINITY : fmaf(mx[m], a.scale * ks_scale, __builtin_amdgcn_logf(l[m]) * kLn2);
             }
         }
         __syncthreads();  // the tiles, ml, odd and o_lds are written again by the next piece
@@ -914,14 +966,17 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
 #pragma unroll
         for (int d = 32; d; d >>= 1) to = fmaxf(to, __shfl_xor(to, d));
         to = fmaxf(to, m);
-        const float f = weight(m, to, cc), g = weight(mk, to, cc);
-        lk *= g;
+        // the rows are means, weighted so that the weights' sum is 1: nothing passes the largest of them
+        float g = lk * weight(mk, to, cc), sum = g;
 #pragma unroll
-        for (int d = 32; d; d >>= 1) lk += __shfl_xor(lk, d);
+        for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+        const float was = l * weight(m, to, cc);
         m = to;
-        l = l * f + lk;
+        l = was + sum;
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        g *= inv;
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] *= f;
+        for (int e = 0; e < N; ++e) o[e] *= was * inv;
         for (int k = 0; k < count; k += 8) {
             if (k) request(k);
 #pragma unroll
@@ -945,22 +1000,23 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
         for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
         l = 0.f;
         m = top;
+        for (int w = 0; w < 4; ++w) l += part[w][D + 1] * weight(part[w][D], top, cc);
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] = 0.f;
         for (int w = 0; w < 4; ++w) {
-            const float f = weight(part[w][D], top, cc);
-            l += part[w][D + 1] * f;
+            const float f = part[w][D + 1] * weight(part[w][D], top, cc) * inv;
 #pragma unroll
             for (int e = 0; e < N; ++e) o[e] = fmaf(part[w][lane * N + e], f, o[e]);
         }
     }
     const int t = r / a.group, hq = h * a.group + (r - t * a.group);
-    const bool any = l > 0.f || l != l;
-    const float inv = any ? (a.c.v_scale ? a.c.v_scale[h] : 1.f) / l : 0.f;
+    const float vs_scale = a.c.v_scale ? a.c.v_scale[h] : 1.f;
     TQ* out = static_cast<TQ*>(a.out) + (int64_t)(s.q0 + t) * a.ldo + (int64_t)hq * D + lane * N;
 #pragma unroll
-    for (int e = 0; e < N; ++e) out[e] = (TQ)(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = any ? fmaf(m, scale, (__builtin_amdgcn_logf(l) - kShift) * kLn2) : -INFINITY;
+    for (int e = 0; e < N; ++e) out[e] = (TQ)(o[e] * vs_scale);
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = l == 0.f ? -INFINITY : fmaf(m, scale, __builtin_amdgcn_logf(l) * kLn2);
 }
 
 template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>

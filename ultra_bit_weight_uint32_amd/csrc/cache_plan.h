@@ -150,7 +150,7 @@ UBW_HD inline void attn_range(int units, int splits, int s, int* u0, int* u1) {
 inline int64_t attn_max_items(int batch, int64_t max_rows, int kv_heads, int head_dim, AttnTile t) {
     return attn_target(t, head_dim) + (int64_t)batch * cdiv(max_rows, attn_rows(t)) * kv_heads;
 }
-// Scratch floats: each piece's rows (head_dim sums, then the running maximum and the sum of weights),
+// Scratch floats: each piece's rows (head_dim means, then the running maximum and the sum of weights),
 // then the cut itself (units per piece, each sequence's first piece); for trees of max_tree tokens or
 // fewer, whose pieces have other sizes.
 inline int64_t attn_workspace_floats(int batch, int max_tree, int group, int kv_heads, int head_dim) {
