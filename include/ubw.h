@@ -496,8 +496,11 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
  * nothing, whatever their values (NaN and infinities included). Query head h reads key/value head
  * h / (heads / kv_heads). Scores, softmax and sums are fp32; the weights are rounded to q's type for
  * the product with v. bf16 queries over an 8-bit cache with head_dim 128 or 256 are multiplied as two
- * 8-bit parts: exact but for elements below 2^-13 of the largest of their 128 dims, which are taken to
- * 2^-22 of it. A query with an infinity counts there as one with a NaN.
+ * 8-bit parts: exact but for elements below 2^-13 of the largest of their 128 dims (of 2^-83 where it is
+ * smaller), which are taken to 2^-22 of it. A query with an infinity counts there as one with a NaN.
+ * bf16 queries take a power of two of the scale along into the product, so that finite scores, and
+ * differences of them, stay in fp32's range with any scale (times k_scale) from 2^-30 on; elements
+ * below 2^-94 may count as 0. Values may have any finite size.
  *   q, out     q_dtype (UBW_F16 or UBW_BF16; the cache's type unless that is UBW_E4M3), token t's
  *              heads x head_dim at q + t * ldq (out + t * ldo), 16-byte aligned rows
  *   q_start    int32 [batch + 1] ascending, q_start[batch] <= tokens; rows of out and lse that

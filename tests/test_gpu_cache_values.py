@@ -9,7 +9,8 @@ import math
 import pytest
 
 import ultra_bit_weight_uint32_amd as ubw
-from test_gpu_cache import BF16, DEV, E4M3, F16, attention_reference, batch_of, cache_of, gen, i32, randn
+from test_gpu_cache import (BF16, DEV, E4M3, F16, attention_reference, batch_of, cache_of, check_attention, gen, i32,
+                            randn)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -228,3 +229,80 @@ def test_bf16_context_values_that_are_not_finite(heads):
         assert (out[..., 5] == math.inf).all() and (out[..., 77] == -math.inf).all() and out[..., 100].isnan().all()
         out[..., [5, 77, 100]] = want[0][..., [5, 77, 100]].to(DEV).to(BF16)
         check_relative(out, lse, want, 1400)
+
+
+# ---------------------------------------------------------------------------------------------
+# scores that are finite where q . k or a difference of two scores is not
+
+@pytest.mark.parametrize("heads", [1, 20, 40, 100])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=str)
+def test_bf16_scores_up_to_the_largest(dtype, dim, heads):
+    """A context of scores 0 with one of +1.5 2^127 and one of -1.75 2^127, whose difference passes fp32, and
+    with q . k of 2^4 to 2^29 times that before the scale, in one product and as a sum of eight: the high one
+    takes all; without it the zeros share, and the low one weighs nothing; alone, the low one is all there
+    is. Zeros are exact, so all weights are 0, 1, or alike."""
+    g = gen(dim + heads)
+    page = 16
+    for first, second in APART:
+        n = max(first, second) + 4
+        for scale in (1.0, 2.0 ** -4, 2.0 ** -29, 8.0):
+            table, pages = batch_of([n - 1], [1], page, g, cols=columns(page, True))
+            cache = cache_of(pages, 1, page, dim, dtype, g, scales=False)
+            at = torch.arange(n, device=DEV)
+            where = (table[0, at // page].long(), 0, at % page)
+            k = torch.zeros((n, dim), device=DEV)
+            # q . k is 3 2^126 and -3.5 2^126 over the scale, in `parts` equal products
+            parts = 8 if second % 2 else 1
+            size = 64.0 if dtype is E4M3 else 2.0 ** 66
+            x = 2.0 ** 126 / scale / size / parts
+            if x >= 2.0 ** 127:
+                continue   # no bf16 query is so large
+            q = torch.zeros((1, heads, dim), dtype=BF16, device=DEV)
+            q[..., 3:3 + parts] = x
+            for case in ("high", "low"):
+                k.zero_()
+                if case == "high":
+                    k[first, 3:3 + parts] = 3.0 * size
+                k[second, 3:3 + parts] = -3.5 * size
+                assert torch.equal(k.to(dtype).float(), k)
+                cache.k[where] = k.to(dtype)
+                v = cache.v[where].double().cpu()
+                for split in (True, False):
+                    out, lse = attend(q, cache, table, [0, 1], [n - 1], scale=scale, split=split)
+                    if case == "high":
+                        assert torch.equal(out[0].double().cpu(), v[first].expand(heads, dim)), (first, second, scale, split)
+                        assert (lse == 1.5 * 2.0 ** 127).all()
+                    else:
+                        rest = [p for p in range(n) if p != second]
+                        want, mean = v[rest].mean(0), v[rest].abs().mean(0)
+                        off = (n + 64) * 2.0 ** -24 * mean
+                        assert ((out[0].double().cpu() - want).abs() <= off + 2.0 ** -8 * (want.abs() + off)).all()
+                        assert ((lse.double() - math.log(n - 1)).abs() <= (n + 64) * 2.0 ** -24 + 2.0 ** -20).all()
+            # a lone position
+            cache.k[table[0, 0].long(), 0, 0] = k[second].to(dtype)
+            out, lse = attend(q, cache, table, [0, 1], [0], scale=scale)
+            assert torch.equal(out[0], cache.v[table[0, 0].long(), 0, 0].to(BF16).expand(heads, dim))
+            assert (lse == -1.75 * 2.0 ** 127).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 1e-3, 0.3, 1.0, 5.0, 1e3, 2.0 ** 20])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3], ids=str)
+def test_scales_of_every_size(dtype, dim, scale):
+    """Queries so large or small that scores are of ordinary size under each scale."""
+    g = gen(dim)
+    ctx, drafts, start = [200, 900], [3, 2], [0, 3, 5]
+    for split in (True, False):
+        table, pages = batch_of(ctx, drafts, 16, g, cols=columns(16, split))
+        cache = cache_of(pages, 2, 16, dim, dtype, g)
+        qt = F16 if dtype is F16 else BF16
+        wide = dim ** -0.5 / scale
+        if dtype is F16 and not 2.0 ** -10 < wide < 2.0 ** 12:
+            continue
+        q = (randn((5, 8, dim), torch.float32, g) * wide).to(qt)
+        out, lse = attend(q, cache, table, start, ctx, None, scale=scale, split=split)
+        want = attention_reference(q, cache, table, start, ctx, None, scale)
+        more = 2.0 ** -22 * scale * q.float().abs().amax(-1).double().cpu() * cache.k.float().abs().sum(-1).max().item() * 1.5 \
+            if dtype is E4M3 else 0.0   # bf16 queries over 8 bits: what their smallest elements may be off by
+        check_attention(out, lse, want, qt, 1024, more)

@@ -94,6 +94,13 @@ struct Half<b16> {
 __device__ inline float weight(float m, float to, float cc) {
     return m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - to) * cc);
 }
+// bf16 queries are multiplied by 2^lower(scale) before the product with the keys, so that what is left of the
+// scale is 4 or more: a finite score is then below 2^126 there, and neither it nor a difference of two passes
+// fp32's range. Down to 2^-32 only, so that elements above 2^-94 lose nothing. (fp16 products stay below 2^41.)
+template <typename T>
+__device__ inline int lower(float scale) {
+    return Half<T>::kSplits ? min(max(__builtin_amdgcn_frexp_expf(scale) - 3, -32), 0) : 0;
+}
 template <typename T>
 __device__ inline uint32_t pack(float a, float b) {  // rounded to nearest even
     typename Half<T>::x2 v;
@@ -294,13 +301,14 @@ __device__ inline uint32_t not_finite(uint32_t w) {
 // Values below 2^-13 of the row's largest are off by up to 2^-22 of it (less than the fp32 sums of a score
 // lose). q[0 .. 1] get hi, q[2 .. 3] lo; returns the parts' powers of two as biased bytes 0 and 1 (one
 // power for the row: the product applies those of its four lanes to 32 of the 128 dims each, and these are
-// not the lanes that hold them). Infinities become NaN, which scores with them end in anyway.
+// not the lanes that hold them; rows below 2^-115 - low count as of that size, so that it fits). Infinities become NaN, which scores with them end in anyway.
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kOne8 = 0x7f;  // the power 2^0
 __device__ inline i32x8 joined(u32x4 a, u32x4 b) {
     return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
-__device__ inline int split_query(u32x4* q) {
+// Returns them times 2^low.
+__device__ inline int split_query(u32x4* q, int low) {
     uint32_t top = 0;  // exponent of the largest, in place
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -310,7 +318,7 @@ __device__ inline int split_query(u32x4* q) {
     }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-    const int e = max((int)(top >> 7), 12);
+    const int e = max((int)(top >> 7), 12 - low);
     const float up = __builtin_bit_cast(float, (uint32_t)(261 - e) << 23);  // 2^(134 - e): the largest comes to [128, 256)
     u32x4 hi[2], lo[2];
 #pragma unroll
@@ -335,7 +343,7 @@ __device__ inline int split_query(u32x4* q) {
     q[1] = hi[1];
     q[2] = lo[0];
     q[3] = lo[1];
-    return (e - 7) | (e - 12) << 8;
+    return (e - 7 + low) | (e - 12 + low) << 8;
 }
 
 // MT row tiles a wave, R waves side by side over rows, T over positions, NS tiles of 32 positions a
@@ -394,7 +402,6 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     const int lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % R, tw = wave / R;
-    const float c2 = a.scale * kLog2e;
 
     int chunk = 0, items;
     const int blocks_max = (a.max_tree * a.group + RB - 1) / RB;
@@ -528,18 +535,32 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 q[m][ks] = r < rows ? *reinterpret_cast<const u32x4*>(at + d * 2) : u32x4{0, 0, 0, 0};
             }
         }
-        int qscale[MT][NG];
-        if constexpr (kSplit)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int g = 0; g < NG; ++g) qscale[m][g] = split_query(&q[m][4 * g]);
         float ks_scale = 1.f, vs_scale = 1.f;
         if constexpr (FP8) {
             if (a.c.k_scale) ks_scale = a.c.k_scale[h];
             if (a.c.v_scale) vs_scale = a.c.v_scale[h];
         }
-        const float cc = c2 * ks_scale;
+        // What the products leave is a score over `unit`, and so are the maxima.
+        const int low = lower<TQ>(a.scale * ks_scale);
+        const float unit = __builtin_bit_cast(
+            float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, ldexpf(a.scale * ks_scale, -low))));
+        const float cc = unit * kLog2e;
+        int qscale[MT][NG];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if constexpr (kSplit) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) qscale[m][g] = split_query(&q[m][4 * g], low);
+            } else if constexpr (Half<TQ>::kSplits) {
+                const float f = ldexpf(1.f, low);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        q[m][ks][i] = pack<TQ>(__builtin_bit_cast(float, q[m][ks][i] << 16) * f,
+                                               __builtin_bit_cast(float, q[m][ks][i] & 0xffff0000u) * f);
+            }
+        }
 
         // The compiler waits for queries and masks here, once, instead of at their first use in the loop, where it
         // would wait for all transfers under way as well.
@@ -825,7 +846,9 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 int e = 1;
 #pragma unroll
                 for (int m = 0; m < MT; ++m) e = max(e, __builtin_amdgcn_frexp_expf(l[m]));
-                shift = (float)(-1 - e);  // l 2^shift < 1/2: sums stay below half of the largest value
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor(e, d));
+                shift = (float)(-1 - __builtin_amdgcn_readfirstlane(e));  // l 2^shift < 1/2: sums stay below half of the largest value
                 again = true;
                 it -= (int)gridDim.x;
                 continue;
@@ -869,7 +892,9 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             odds = __builtin_amdgcn_readfirstlane(odds);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int rl = (rw * MT + m) * 16 + c, r = blk * RB + rl;
+                int rl = (rw * MT + m) * 16 + c;
+                asm volatile("" : "+v"(rl));  // addresses from it are not kept through the loops (two instances would spill)
+                const int r = blk * RB + rl;
                 if (r >= rows) continue;
 #pragma unroll
                 for (int w = 0; w < T - 1; ++w)
@@ -913,7 +938,7 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                         u32x2{pack<TQ>(o[m][e][0] * f, o[m][e][1] * f), pack<TQ>(o[m][e][2] * f, o[m][e][3] * f)};
                 if (a.lse && j == 0)
                     a.lse[(int64_t)(s.q0 + t) * a.heads + hq] =
-                        l[m] == 0.f ? -INFINITY : fmaf(mx[m], a.scale * ks_scale, __builtin_amdgcn_logf(l[m]) * kLn2);
+                        l[m] == 0.f ? -INFINITY : fmaf(mx[m], unit, __builtin_amdgcn_logf(l[m]) * kLn2);
             }
         }
         __syncthreads();  // the tiles, ml, odd and o_lds are written again by the next piece
@@ -938,7 +963,8 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
     const int blk = r / rb, rl = r - blk * rb;
     const int first = before + h * p.splits * p.blocks + blk;
     const int s0 = WAVES == 4 ? wave : 0;
-    const float scale = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.f), cc = scale * kLog2e;
+    const float scale = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.f);
+    const float unit = ldexpf(scale, -lower<TQ>(scale)), cc = unit * kLog2e;  // as in k_attn
     float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = 0.f;
@@ -1016,7 +1042,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, int rb) {
 #pragma unroll
     for (int e = 0; e < N; ++e) out[e] = (TQ)(o[e] * vs_scale);
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = l == 0.f ? -INFINITY : fmaf(m, scale, __builtin_amdgcn_logf(l) * kLn2);
+        a.lse[(int64_t)(s.q0 + t) * a.heads + hq] = l == 0.f ? -INFINITY : fmaf(m, unit, __builtin_amdgcn_logf(l) * kLn2);
 }
 
 template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE>
