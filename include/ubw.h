@@ -463,8 +463,9 @@ typedef struct ubw_kv_cache {
  *      (a cos - b sin, b cos + a sin); dims from rot on stay y. Pairs are (i, i + rot / 2), or with
  *      interleaved != 0 (2 i, 2 i + 1). Angles are taken in 64 bits, so far positions stay exact.
  *   q_out[t][h] = z of q;  cache.k at slot slots[t] = z of k;  cache.v there = v.
- * Norm and rotation are computed in fp32 and rounded once, to nearest even; e4m3 elements are
- * value / scale[h], values beyond 448 become 448 of their sign, a NaN stays a NaN.
+ * Norm and rotation are computed in fp32 (heads whose squares pass its range by a power of two of
+ * theirs) and rounded once, to nearest even; e4m3 elements are value / scale[h], values beyond 448
+ * become 448 of their sign, a NaN stays a NaN.
  *   q, k, v    in_dtype (UBW_F32, UBW_F16, UBW_BF16), token t's heads x head_dim values at
  *              q + t * ldq (ldk, ldv), contiguous; rows 16-byte aligned (rows of a fused buffer do)
  *   q_weight, k_weight  fp32 [head_dim] or NULL (no norm)

@@ -10,7 +10,7 @@ import pytest
 
 import ultra_bit_weight_uint32_amd as ubw
 from test_gpu_cache import (BF16, DEV, E4M3, F16, attention_reference, batch_of, cache_of, check_attention, gen, i32,
-                            randn)
+                            near, randn, rope_reference)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -306,3 +306,30 @@ def test_scales_of_every_size(dtype, dim, scale):
         more = 2.0 ** -22 * scale * q.float().abs().amax(-1).double().cpu() * cache.k.float().abs().sum(-1).max().item() * 1.5 \
             if dtype is E4M3 else 0.0   # bf16 queries over 8 bits: what their smallest elements may be off by
         check_attention(out, lse, want, qt, 1024, more)
+
+
+# ---------------------------------------------------------------------------------------------
+# the norm of large and small heads
+
+@pytest.mark.parametrize("pairs", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, BF16], ids=str)
+def test_norm_of_heads_of_every_size(dtype, dim, pairs):
+    """Heads whose squares pass fp32's range above and below, beside ordinary ones in the same wave."""
+    g = gen(dim)
+    t, heads, kv = 9, 6, 2
+    q, k, v = (randn((t, n, dim), torch.float32, g) for n in (heads, kv, kv))
+    for x in (q, k):
+        x.clamp_(-2.9, 2.9)
+        x *= torch.exp2(torch.tensor([0.0, 70, 100, 126, -70, -100, -120, 63, -40], device=DEV))[:, None, None]
+        x[0, 1] *= 2.0 ** 90
+        x[0, 0] *= 2.0 ** -90
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    cache = ubw.KVCache(*(torch.zeros((1, kv, 16, dim), dtype=BF16, device=DEV) for _ in "kv"))
+    w = torch.rand(dim, device=DEV, generator=g) + 0.5
+    freq = torch.exp2(-torch.arange(dim // 4, device=DEV).float() / 8)
+    pos = slots = i32(list(range(t)))
+    for eps in (0.0, 1e-6, 1e-31):
+        out = ubw.qk_norm_rope(q, k, v, cache, pos, slots, freq, q_weight=w, k_weight=w, eps=eps, interleaved=pairs)
+        near(out, *rope_reference(q, w, eps, pos, freq, dim // 2, pairs), BF16)
+        near(cache.k[0, :, :t].transpose(0, 1), *rope_reference(k, w, eps, pos, freq, dim // 2, pairs), BF16)

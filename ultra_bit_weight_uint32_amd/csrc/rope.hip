@@ -135,12 +135,30 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int heads_per_wg) {
         }
         const float* w = isv ? nullptr : isq ? a.qw : a.kw;
         if (w && live) {
-            float ss = 0.f;
+            const auto mean_square = [&] {
+                float ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) ss = fmaf(x[i], x[i], ss);
+                for (int i = 0; i < NE; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-            for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor(ss, m, 16);
-            const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+                for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor(ss, m, 16);
+                return ss * (1.f / D);
+            };
+            float mean = mean_square() + a.eps;
+            if (!(mean > 1e-30f && mean < 1e38f)) {
+                // squares near the ends of fp32 (alike in a head's 16 lanes): of x 2^-e, with eps 2^-2e, where the
+                // larger of them comes near 1
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < NE; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 16));
+                int e = __builtin_amdgcn_frexp_expf(top);
+                if (a.eps > 0.f) e = max(e, (__builtin_amdgcn_frexp_expf(a.eps) + 1) >> 1);
+#pragma unroll
+                for (int i = 0; i < NE; ++i) x[i] = ldexpf(x[i], -e);
+                mean = mean_square() + ldexpf(a.eps, -2 * e);
+            }
+            const float r = 1.f / sqrtf(mean);
             float g[NE];
             load_row<float, NE>(w + d0, g);
 #pragma unroll
