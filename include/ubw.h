@@ -493,8 +493,9 @@ int ubw_qk_norm_rope(const ubw_kv_cache* cache, const void* q, int64_t ldq, cons
  * L + i (stored by ubw_qk_norm_rope before). Token i sees every position below L, and position
  * L + j (j < n) where bit j of masks[q_start[b] + i] is set (masks NULL: where j <= i).
  *   s_j = scale * q . k_j over the positions seen;  out = sum softmax(s)_j v_j;  lse = log sum exp s
- * A token that sees nothing gets out = 0 and lse = -infinity. Positions not seen contribute
- * nothing, whatever their values (NaN and infinities included). Query head h reads key/value head
+ * A token that sees nothing (or only scores of -infinity) gets out = 0 and lse = -infinity. Positions
+ * not seen contribute nothing, whatever their values (NaN and infinities included). An infinite value in
+ * the context counts as NaN where its weight rounds to 0. Query head h reads key/value head
  * h / (heads / kv_heads). Scores, softmax and sums are fp32; the weights are rounded to q's type for
  * the product with v. bf16 queries over an 8-bit cache with head_dim 128 or 256 are multiplied as two
  * 8-bit parts: exact but for elements below 2^-13 of the largest of their 128 dims (of 2^-83 where it is

@@ -15,15 +15,16 @@
 //     the same eight positions of its dim; value rows lie with their 16-byte columns exchanged by XOR so
 //     that these reads spread over the banks. 8-bit values are read so too and widened on the way; 8-bit
 //     keys are widened as well, or (bf16 queries, 128 dims or more) multiplied as they are by queries in
-//     two 8-bit parts, which costs the matrix cores the same and the vector unit nothing: 512 rows 520 -> 455 us.
+//     two 8-bit parts, which costs the matrix cores the same and the vector unit nothing: 4 trees of 64 tokens
+//     over 30K to 65K positions (512 rows of a head) 520 -> 455 us.
 //   * m is not followed exactly: o is scaled only when a score passes m by more than 2^8 (a wave-uniform
 //     branch that long contexts take a few times), so the usual step has no cross-lane work at all, l is
 //     kept per lane, and fp16 weights p = 2^((s - m) log2 e + 7) stay below 2^15, inside fp16, while those down
-//     to 2^-21 of the largest are normal numbers (bf16 ones have fp32's range and no shift). m is kept as a score and -m is what the product K Q^T
-//     starts from, so that s - m costs nothing and is right at any size of s (s log2 e - m in one fused
-//     step, m rounded, is off by the rounding of m: at |s| = 10^8 the largest weight would be 2^(7 +- 4)).
-//     Waves and pieces are joined by differences of these maxima too, and as means of values, which never pass
-//     the largest value.
+//     to 2^-21 of the largest are normal numbers (bf16 ones have fp32's range and no shift). m is kept as a score
+//     and -m is what the product K Q^T starts from, so that s - m costs nothing and is right at any size of s
+//     (s log2 e - m in one fused step, m rounded, is off by the rounding of m: at |s| = 10^8 the largest weight
+//     would be 2^(7 +- 4)). Waves and pieces are joined by differences of these maxima too, and as means of
+//     values, which never pass the largest value.
 // Descriptors cover 16 rows; one of size 0 stands for rows that are not needed or on no valid page, so
 // every step issues the same transfers, their count is waited for exactly, and no table entry is ever
 // trusted. Few rows (R = 1): each wave has tiles of its own and no barrier; with one tile, its keys make
@@ -32,17 +33,18 @@
 // share each step, double-buffered, one barrier a step of 64 positions.
 // Nothing in the loop is a vector load the compiler knows of (the block table is read by the scalar
 // unit, the queries are waited for before): it would wait for it, and so for all transfers under way
-// (1.0 GB at 128 rows: 226 us with such waits, 170 without).
+// (1.0 GB at 128 rows: 226 us with such waits, 170 without). No instance spills vector registers with the flags
+// of the build (packed fp32 off), so no scratch access is among the loop's loads either.
 //
 // Split over workgroups: the pieces (sequence, head, row block, run of positions) are cut on the
 // device from the lengths, of equal size, and taken by a grid of resident workgroups; a piece that is not
 // a whole sequence leaves o / l, m, l in the workspace and k_join weighs them in order. Few rows take about
-// three pieces a workgroup where each is long enough (64 ragged sequences: 249 against 269 us), many rows
-// one (their sums are large: 170 against 198 us).
+// three pieces a workgroup where each is long enough (64 ragged sequences, with the join: 236 against 272 us),
+// many rows one (their sums are large: 8 trees of 16 tokens 185 against 220 us).
 //
 // Bound: HBM up to about 64 rows (5.0 to 5.8 TB/s of keys and values over long contexts, where a plain
 // streaming read of this card reaches 6.4); beyond, the vector unit beside the matrix cores (1.0 PFLOP/s
-// at 512 rows of 128 dims in 8 bits); short contexts, a chain of a dozen memory latencies (10 us).
+// at 512 rows of 128 dims in 8 bits); short contexts, a chain of a dozen memory latencies (7 to 8 us).
 #include "cache_internal.h"
 
 namespace ubw {
@@ -354,8 +356,8 @@ struct Cfg {
     static constexpr int kTiles = T * NB * NS * Layout<FP8, D>::kBytes;
     static constexpr int kJoin = (T - 1) * RB * (D + 4) * 4;  // laid over the tiles
     static constexpr int kLds = kTiles > kJoin ? kTiles : kJoin;
-    // workgroups per CU: by LDS, and waves per SIMD by registers (with three waves the largest tiles spill: 64 rows of 8
-    // bits over 16K positions of 8 sequences 111 us, with two 68)
+    // workgroups per CU: by LDS, and waves per SIMD by registers (with three waves the largest tiles spill: 8 bits,
+    // 8 tokens of 8 sequences over 16K positions, 64 heads over 8 of 128 dims: 111 us, with two 68)
     static constexpr int kFit = (160 * 1024 - 512) / (kLds + 8 * T * RB + 1024);
     static constexpr int kWaves = D * MT == 256 ? 2 : 3;
     static constexpr int kMost = kWaves * 256 / kThreads;
@@ -625,7 +627,8 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             return r;
         };
         const auto scores = [&](uint32_t at, f32x4 (&sc)[MT][2 * NS]) {
-            // read ahead of the products, as the values below (512 rows of 8 bits, fp16 queries 253 -> 235 us with both)
+            // read ahead of the products, as the values below (with both: eight trees of 64 tokens over 12K
+            // positions, 64 heads over 8 of 128 dims, fp16 queries over 8-bit keys 253 -> 235 us)
             constexpr int AHEAD = kSplit || NK < 4 ? 2 : 4;
             static_assert(AHEAD <= NK, "reads stay inside the step");
             Keys raw[AHEAD];
@@ -734,8 +737,9 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 }
             }
             // The reads of the first values go out before the weights are computed, each of the others four
-            // products ahead (left to itself the compiler waits for every read behind its request: four 64-token
-            // trees over 12K positions of 256 dims in 8 bits 317 us, 258 so; of 128 dims 238 and 231).
+            // products ahead (left to itself the compiler waits for every read behind its request: trees of 64
+            // tokens over 12K positions, 64 heads over 8, in 8 bits: four of 256 dims 317 us, 258 so; eight of 128
+            // dims 238 and 231).
             constexpr int AHEAD = 4, NV = NS * NE;
             static_assert(AHEAD <= NV, "reads stay inside the step");
             Values raw[AHEAD];
@@ -848,7 +852,8 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
                 for (int m = 0; m < MT; ++m) e = max(e, __builtin_amdgcn_frexp_expf(l[m]));
 #pragma unroll
                 for (int d = 1; d < 16; d <<= 1) e = max(e, __shfl_xor(e, d));
-                shift = (float)(-1 - __builtin_amdgcn_readfirstlane(e));  // l 2^shift < 1/2: sums stay below half of the largest value
+                // l 2^shift < 1/2: sums stay below half of the largest value
+                shift = (float)(-1 - __builtin_amdgcn_readfirstlane(e));
                 again = true;
                 it -= (int)gridDim.x;
                 continue;
@@ -1055,7 +1060,9 @@ hipError_t launch(const AttnArgs& a, AttnTile t, hipStream_t s) {
     const unsigned lds = a.target > 0 ? (unsigned)(a.batch + 1) * 4 : 0;
     k_attn<TQ, FP8, D, MT, R, T, NS, NB, ONCE><<<(unsigned)wgs, C::kThreads, lds, s>>>(a);
     if (a.target > 0) {
-        // few rows: many pieces each, four waves share them
+        // Few rows: many pieces each, four waves share them. Both launches with one wave and with four, 64 heads over
+        // 8 of 128 dims: one token over 32K positions 36.7 and 35.1 us, 16 tokens (1024 rows) 49.7 and 49.0, over 2000
+        // 20.0 and 20.7; two trees of 16 over 8000 36.9 and 37.3, eight over 1500 36.2 and 46.9. Of 64 and 256 dims alike.
         if (rows * pairs <= 1024)
             k_join<TQ, D, 4><<<dim3((unsigned)pairs, (unsigned)rows), 256, 0, s>>>(a, C::RB);
         else
@@ -1067,7 +1074,7 @@ template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const AttnArgs& a, AttnTile t, hipStream_t s) {
     const bool one_block = a.max_tree * a.group <= attn_rows(t);
     if constexpr (D == 256) {
-        // 16 bits: 8 sequences of 16K positions with NB = 1 96 us, with 2 (one workgroup a CU) 132
+        // 16 bits: 8 sequences of 16K positions, 4 key/value heads, with NB = 1 96 us, with 2 (one workgroup a CU) 132
         if (t.row_waves == 1) return launch<TQ, FP8, D, 1, 1, 2, 1, FP8 ? 2 : 1, true>(a, t, s);
         return one_block ? launch<TQ, FP8, D, 1, 4, 1, 1, 2, true>(a, t, s) : launch<TQ, FP8, D, 1, 4, 1, 1, 2, false>(a, t, s);
     } else {

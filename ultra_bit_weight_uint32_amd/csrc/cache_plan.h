@@ -103,14 +103,20 @@ inline AttnTile attn_tile(int64_t max_rows, int head_dim) {
 }
 
 // Contexts of up to this many positions (with their tokens) are not split: a few more steps of one
-// workgroup take less than cutting the batch and joining its pieces in a second launch. By the positions
-// a workgroup takes in one step: 128 with one row wave (64 dims and 128), of 256 dims 64; two row waves
-// 64, four 64 and of 256 dims 32. 128 dims of 16 bits, split and not, for one sequence and for eight:
-// 8 rows at 500 positions 13.6 and 11.2 us, 15.2 and 12.7, at 760 13.8 and 13.5, 18.2 and 16.2, at 1000
-// 13.7 and 15.7, 18.3 and 19.9; 64 rows at 380 16.9 and 17.2, 21.8 and 18.1, at 760 16.7 and 23.1, 28.5 and
-// 24.8; 128 rows at 200 18.7 and 16.2, 25.1 and 16.5, at 380 19.4 and 22.6, 28.9 and 22.9. 256 dims, 8 rows
-// at 200 17.5 and 16.2, at 380 17.6 and 20.6. So many rows of 64 and more (sequence, key/value head) pairs,
-// which use a quarter of the card as they are, have twice the limit.
+// workgroup take less than cutting the batch and joining its pieces in a second launch. The limit goes by
+// the positions that a workgroup takes in one step: 128 with one row wave (64 dims and 128), of 256 dims 64;
+// two row waves 64, four 64 and of 256 dims 32. Times in us split / not, one sequence and (behind the
+// semicolon) eight, 8 key/value heads, 16 bits:
+//   128 dims:   8 rows at 500 positions 13.4 / 10.6; 15.0 / 12.0, at 760 13.5 / 12.9; 17.6 / 15.8, at 1000 13.4 / 15.2; 18.1 / 18.9
+//              48 rows at 380 16.0 / 15.8; 19.6 / 16.4, at 760 16.0 / 20.9; 25.1 / 23.3
+//             128 rows at 250 18.5 / 17.1; 27.0 / 17.5, at 380 18.8 / 20.5; 28.3 / 21.1, at 500 18.8 / 23.8; 34.3 / 24.5
+//    64 dims:   8 rows at 760 12.0 / 9.8; 14.5 / 10.2, at 1000 11.9 / 11.1; 14.6 / 12.2
+//              48 rows at 380 13.8 / 11.7; 15.9 / 12.0, at 760 13.9 / 15.3; 18.3 / 15.6
+//             128 rows at 250 15.9 / 13.1; 20.8 / 13.3, at 380 16.2 / 15.7; 21.8 / 16.1
+//   256 dims:   8 rows at 250 17.0 / 15.3; 18.6 / 15.9, at 380 17.1 / 19.0; 19.4 / 19.8
+//              48 rows at 120 15.9 / 11.7; 16.2 / 12.0, at 250 18.3 / 16.7; 21.9 / 17.5
+// 64 (sequence, key/value head) pairs or more, as the eight sequences here, use a quarter of the card
+// without a split; for them the limit of more than 32 rows (64 and 128 dims) is twice as high.
 inline int attn_unsplit(AttnTile t, int head_dim, int64_t pairs) {
     if (head_dim == 256) return t.row_waves == 1 ? 256 : 128;
     return t.row_waves == 1 ? 768 : (t.row_waves == 2 ? 384 : 256) * (pairs >= 64 ? 2 : 1);

@@ -51,9 +51,10 @@ __global__ __launch_bounds__(256) void k_copy_pages(Pages c, int layers, int lro
 // ---- drawing kept tokens together: a workgroup takes 256 16-byte columns of a sequence's rows (a
 // column: one 16 bytes of one head's rows in one layer, keys or values). Where each kept row comes from
 // and goes to is looked up once, by 256 threads in parallel, into LDS (looked up by every thread in turn
-// the same moves, 31 MB in 80 layers, took 19 us instead of 14.6). Then a thread moves its column row by row,
-// kMove at a time: a kept token's index is at least its place, so the rows read lie at or behind the rows
-// written and nothing is overwritten unread; threads do not share columns. Both sides pass the caches by
+// the same moves, 31 MB in 80 layers, took 19 us instead of 14.6 while they still went through the
+// caches). Then a thread moves its column row by row, kMove at a time: a kept token's index is at least its
+// place, so the rows read lie at or behind the rows written and nothing is overwritten unread; threads do
+// not share columns. Both sides pass the caches by
 // (15.0 -> 11.5 us: nothing is left in them for the kernel's end to write back).
 constexpr int kMove = 16;
 
