@@ -153,3 +153,41 @@ def test_a_captured_split_call_beside_eager_ones():
         eager = ubw.tree_attn(q, cache, table, start, ctx, workspace=ws[0], **args)
         torch.cuda.synchronize()
         assert torch.equal(out, eager), lens
+
+
+def test_masks_and_tables_in_their_other_forms():
+    """A table whose rows lie apart, masks as uint64, queries and outputs that are parts of larger buffers, and
+    outputs written over the queries: the results of the plain call."""
+    g = gen(23)
+    for tokens, heads, dt, dim in ((4, 8, F16, 128), (9, 40, BF16, 64), (3, 6, BF16, 256)):
+        ctx, drafts, start = [1300, 77], [tokens, tokens], [0, tokens, 2 * tokens]
+        table, pages = batch_of(ctx, drafts, 16, g)
+        cache = cache_of(pages, 2, 16, dim, dt, g)
+        q = randn((2 * tokens, heads, dim), dt, g)
+        masks = torch.randint(-2 ** 63, 2 ** 63 - 1, (2 * tokens,), device=DEV, generator=g)
+        want = split_call(q, cache, table, start, ctx, masks)
+        apart = torch.nn.functional.pad(table, (2, 5), value=10 ** 6)[:, 2:-5]
+        assert not apart.is_contiguous()
+        for split in (True, False):
+            ws = ubw.tree_attn_workspace(2, tokens, heads, 2, dim, DEV) if split else None
+            wide = torch.zeros((2 * tokens, heads + 3, dim), dtype=dt, device=DEV)
+            wide[:, 1:-2] = q
+            got = ubw.tree_attn(wide[:, 1:-2], cache, apart, i32(start), i32(ctx), masks.view(torch.uint64), max_tree=tokens,
+                                workspace=ws, out=torch.full_like(wide, 77)[:, 2:-1])
+            plain = ubw.tree_attn(q, cache, table, i32(start), i32(ctx), masks, max_tree=tokens, workspace=ws)
+            assert torch.equal(got, plain) and (not split or torch.equal(got, want[0]))
+            over = q.clone()
+            ubw.tree_attn(over, cache, table, i32(start), i32(ctx), masks, max_tree=tokens, workspace=ws, out=over)
+            assert torch.equal(over, plain)
+
+
+def test_a_thousand_heads_over_one():
+    g = gen(24)
+    table, pages = batch_of([900, 5], [1, 2], 16, g)
+    for dt, ct in ((F16, E4M3), (BF16, BF16)):
+        cache = cache_of(pages, 1, 16, 64, ct, g)
+        q = randn((3, 1024, 64), dt, g)
+        out, lse = split_call(q, cache, table, [0, 1, 3], [900, 5])
+        for h in (0, 127, 128, 1023):
+            want = attention_reference(q[:, h:h + 1].contiguous(), cache, table, [0, 1, 3], [900, 5], None)
+            check_attention(out[:, h:h + 1], lse[:, h:h + 1], want, dt, 1000)

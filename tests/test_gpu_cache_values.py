@@ -333,3 +333,60 @@ def test_norm_of_heads_of_every_size(dtype, dim, pairs):
         out = ubw.qk_norm_rope(q, k, v, cache, pos, slots, freq, q_weight=w, k_weight=w, eps=eps, interleaved=pairs)
         near(out, *rope_reference(q, w, eps, pos, freq, dim // 2, pairs), BF16)
         near(cache.k[0, :, :t].transpose(0, 1), *rope_reference(k, w, eps, pos, freq, dim // 2, pairs), BF16)
+
+
+@pytest.mark.parametrize("heads", [2, 20, 40, 70])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_bf16_values_here_and_there(dim, heads):
+    """More sequences than workgroups, every third with values up to the largest (its piece is gone through
+    twice), one with an infinity: each is right whatever its workgroup did before; in a replayed graph too."""
+    g = gen(heads + dim)
+    seqs, page = 1600, 16
+    ctx = torch.randint(0, 90, (seqs,), generator=torch.Generator().manual_seed(heads)).tolist()
+    table, pages = batch_of(ctx, [1] * seqs, page, g)
+    cache = cache_of(pages, 1, page, dim, BF16, g)
+    for b in range(0, seqs, 3):
+        rows = table[b][table[b] >= 0].long()
+        cache.v[rows] = torch.where(cache.v[rows] < 0, -1.0, 1.0).to(BF16) * torch.finfo(BF16).max
+    cache.v[table[7, 0].long(), 0, 0, 3] = math.inf
+    q = randn((seqs, heads, dim), BF16, g)
+    start = list(range(seqs + 1))
+    out, lse = attend(q, cache, table, start, ctx)
+    assert (out[7, :, 3] == math.inf).all()
+    out[7, :, 3] = 0
+    assert torch.isfinite(out).all()
+    cache.v[table[7, 0].long(), 0, 0, 3] = 0
+    for b in (0, 1, 2, 3, 6, 7, 8, 300, 301, 511, 512, 513, 766, 768, 769, 1023, 1024, 1025, 1300, 1536, 1598, 1599):
+        want = attention_reference(q[b:b + 1], cache, table[b:b + 1], [0, 1], [ctx[b]], None)
+        if b == 7:
+            want[0][..., 3] = 0   # looked at above
+        check_relative(out[b:b + 1], lse[b:b + 1], want, 91)
+    st, cl = i32(start), i32(ctx)
+    again, graph = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ubw.tree_attn(q, cache, table, st, cl, max_tree=1, out=again)
+    for _ in range(3):
+        again.fill_(77)
+        graph.replay()
+        eager = ubw.tree_attn(q, cache, table, st, cl, max_tree=1)
+        torch.cuda.synchronize()
+        assert torch.equal(again, eager)
+
+
+def test_large_bf16_values_in_some_pieces():
+    """Long contexts whose pieces are gone through twice in some places, several pieces a workgroup."""
+    g = gen(5)
+    page, ctx, drafts, start = 256, [90000, 70000], [2, 1], [0, 2, 3]
+    table, pages = batch_of(ctx, drafts, page, g)
+    for heads, dim in ((8, 64), (24, 128), (320, 64)):
+        cache = cache_of(pages, 8, page, dim, BF16, g)
+        for p in (3, 77, 78, 200, 350):
+            cache.v[table[0, p].long()] *= 2.0 ** 125
+        q = randn((3, heads, dim), BF16, g)
+        out, lse = attend(q, cache, table, start, ctx, split=True)
+        assert torch.isfinite(out).all()
+        for h in (0, heads - 1):
+            hk = h // (heads // 8)
+            one = ubw.KVCache(cache.k[:, hk:hk + 1].contiguous(), cache.v[:, hk:hk + 1].contiguous())
+            want = attention_reference(q[:, h:h + 1].contiguous(), one, table, start, ctx, None)
+            check_relative(out[:, h:h + 1], lse[:, h:h + 1], want, 90002)
