@@ -532,6 +532,32 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
                   float scale, void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * ubw_tree_attn for sequences that have the beginning of their contexts in common (samples of one prompt,
+ * requests behind one system prompt: what ubw_pages_fork shares). Group g is the sequences group_start[g] ..
+ * group_start[g + 1] - 1, which hold the same keys and values at positions 0 .. prefix_len[g] - 1; these are
+ * read once for the whole group, by the table row of its first sequence that has tokens. A sequence's other
+ * positions are read by its own row, and so are the last up to 15 of a prefix that is no multiple of 16, and
+ * all positions of a sequence in no group. A prefix_len that passes the shortest context of the group's
+ * sequences (those that have tokens) counts as that context, one below 0 as 0. Results are those of
+ * ubw_tree_attn, up to the order of summing.
+ *   group_start  int32 [groups + 1] ascending, prefix_len int32 [groups]; groups at most UBW_MAX_SEQS
+ *                (0: both may be NULL)
+ *   workspace    ubw_prefix_attn_workspace_bytes() bytes, for as many tokens as the call has or more; always
+ *                needed. It needs no initialization and keeps nothing between calls; calls that may run at the
+ *                same time need their own.
+ *   Everything else as ubw_tree_attn. (Where q_start does not ascend nothing is shared.)
+ * tokens = 0 or batch = 0 enqueues nothing.
+ * Errors: as ubw_tree_attn; UBW_ERANGE (groups, tokens * heads / kv_heads above 2^30).
+ */
+int ubw_prefix_attn_workspace_bytes(int batch, int groups, int64_t tokens, int max_tree, int heads, int kv_heads,
+                                    int head_dim, size_t* out);
+int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+                    const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
+                    int table_cols, const int32_t* group_start, const int32_t* prefix_len, int groups, int max_tree,
+                    int64_t max_len, const uint64_t* masks, float scale, void* out, int64_t ldo, float* lse, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/*
  * Copies whole pages, keys and values of every layer: page pairs[i][0] to page pairs[i][1]. A pair
  * with an entry outside [0, pages) is skipped. No page may be the target of two pairs, or the
  * target of one and the source of another (its contents are then unspecified; nothing else is).

@@ -35,7 +35,8 @@ EXPORTS = (
     "ubw_check_indices", "ubw_extract_patterns", "ubw_lut_gemv_geometry", "ubw_bench_stream_read",
     "ubw_lut_gemv_multi", "ubw_lut_gemv_gs", "ubw_fit_workspace_bytes", "ubw_fit_bases",
     "ubw_gram", "ubw_saliency_workspace_bytes", "ubw_hessian_saliency",
-    "ubw_qk_norm_rope", "ubw_tree_attn_workspace_bytes", "ubw_tree_attn", "ubw_cache_copy_pages",
+    "ubw_qk_norm_rope", "ubw_tree_attn_workspace_bytes", "ubw_tree_attn",
+    "ubw_prefix_attn_workspace_bytes", "ubw_prefix_attn", "ubw_cache_copy_pages",
     "ubw_cache_compact", "ubw_pages_init", "ubw_pages_trim", "ubw_pages_fork", "ubw_pages_reserve",
 )
 
@@ -118,6 +119,8 @@ def lib():
         "ubw_qk_norm_rope": ([C, P, I64, P, I64, P, I64, I, I64, I, P, P, F, P, I, I, P, P, P, I, I64, P], I),
         "ubw_tree_attn_workspace_bytes": ([I, I, I, I, I, ctypes.POINTER(SZ)], I),
         "ubw_tree_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, I, I64, P, F, P, I64, P, P, SZ, P], I),
+        "ubw_prefix_attn_workspace_bytes": ([I, I, I64, I, I, I, I, ctypes.POINTER(SZ)], I),
+        "ubw_prefix_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, P, P, I, I, I64, P, F, P, I64, P, P, SZ, P], I),
         "ubw_cache_copy_pages": ([C, P, I64, P], I),
         "ubw_cache_compact": ([C, P, I64, I, P, P, I, I, P], I),
         "ubw_pages_init": ([PP, P], I),
@@ -637,7 +640,7 @@ def bench_stream_read(buf, nbytes: int, out):
 # keys and values in a paged cache (cache.py, loaded with torch on first use)
 
 _CACHE_CALLS = ("KVCache", "PagePool", "cache_compact", "cache_copy_pages", "page_pool", "pages_fork", "pages_reserve",
-                "pages_trim", "qk_norm_rope", "tree_attn", "tree_attn_workspace")
+                "pages_trim", "prefix_attn", "prefix_attn_workspace", "qk_norm_rope", "tree_attn", "tree_attn_workspace")
 
 
 def __getattr__(name):

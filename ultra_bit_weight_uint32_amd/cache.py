@@ -177,15 +177,8 @@ def tree_attn_workspace(batch, max_tree, heads, kv_heads, head_dim, device="cuda
     return torch.empty(-(-n.value // 4), dtype=torch.float32, device=device)
 
 
-def tree_attn(q, cache, table, q_start, ctx_len, masks=None, *, max_tree, max_len=0, scale=None, out=None, lse=None,
-              workspace=None):
-    """Attention of each sequence's new tokens (one, or a tree of up to 64 drafted ones) over its context
-    in the cache and over one another. q [tokens, heads, head_dim]; table int32 [batch, columns] (rows
-    may be apart); q_start int32 [batch + 1]; ctx_len int32 [batch]; masks int64 or uint64 [tokens], bit
-    j of a token's: it sees token j of its tree (None: those up to itself). max_tree: the most tokens a
-    sequence has; max_len: the longest context plus tokens (0: unknown). lse: None or fp32 [tokens,
-    heads] to be written. workspace: tree_attn_workspace() (None: long contexts are not split over
-    workgroups). Returns out [tokens, heads, head_dim] in q's type."""
+def _attn_args(q, cache, table, q_start, ctx_len, masks, scale, out, lse):
+    """What the attention calls check alike: (out, (q .. table_cols), masks, scale, (out, ldo, lse))."""
     dev, dim = cache.index, cache.head_dim
     qp, ldq, t, heads = _rows(q, "q", dev, dim)
     dtype = q.dtype
@@ -201,13 +194,51 @@ def tree_attn(q, cache, table, q_start, ctx_len, masks=None, *, max_tree, max_le
         if masks.dtype is not torch.int64 and masks.dtype is not torch.uint64:
             raise TypeError(f"masks has dtype {masks.dtype}, expected int64 or uint64")
         masks = _flat(masks, "masks", masks.dtype, dev, t)
-    ws, wsb = None, 0
-    if workspace is not None:
-        ws, wsb = _flat(workspace, "workspace", workspace.dtype, dev), workspace.nbytes
-    _launch("ubw_tree_attn", dev, cache.ref, qp, _TYPES[dtype], ldq, t, heads,
-            _flat(q_start, "q_start", i32, dev, batch + 1), _flat(ctx_len, "ctx_len", i32, dev), batch, tp, ld_table, cols,
-            max_tree, max_len, masks, dim ** -0.5 if scale is None else scale, op, ldo,
-            None if lse is None else _flat(lse, "lse", torch.float32, dev, shape=(t, heads)), ws, wsb)
+    return (out, (cache.ref, qp, _TYPES[dtype], ldq, t, heads, _flat(q_start, "q_start", i32, dev, batch + 1),
+                  _flat(ctx_len, "ctx_len", i32, dev), batch, tp, ld_table, cols),
+            (masks, dim ** -0.5 if scale is None else scale, op, ldo,
+             None if lse is None else _flat(lse, "lse", torch.float32, dev, shape=(t, heads))))
+
+
+def _scratch(workspace, index):
+    """(pointer, bytes) of a workspace, or of none."""
+    return (None, 0) if workspace is None else (_flat(workspace, "workspace", workspace.dtype, index), workspace.nbytes)
+
+
+def tree_attn(q, cache, table, q_start, ctx_len, masks=None, *, max_tree, max_len=0, scale=None, out=None, lse=None,
+              workspace=None):
+    """Attention of each sequence's new tokens (one, or a tree of up to 64 drafted ones) over its context
+    in the cache and over one another. q [tokens, heads, head_dim]; table int32 [batch, columns] (rows
+    may be apart); q_start int32 [batch + 1]; ctx_len int32 [batch]; masks int64 or uint64 [tokens], bit
+    j of a token's: it sees token j of its tree (None: those up to itself). max_tree: the most tokens a
+    sequence has; max_len: the longest context plus tokens (0: unknown). lse: None or fp32 [tokens,
+    heads] to be written. workspace: tree_attn_workspace() (None: long contexts are not split over
+    workgroups). Returns out [tokens, heads, head_dim] in q's type."""
+    out, first, last = _attn_args(q, cache, table, q_start, ctx_len, masks, scale, out, lse)
+    _launch("ubw_tree_attn", cache.index, *first, max_tree, max_len, *last, *_scratch(workspace, cache.index))
+    return out
+
+
+def prefix_attn_workspace(batch, groups, tokens, max_tree, heads, kv_heads, head_dim, device="cuda"):
+    """Scratch for prefix_attn calls of these sizes, with this many tokens in all or fewer (reusable on one stream)."""
+    n = ctypes.c_size_t()
+    _check("ubw_prefix_attn_workspace_bytes", lib().ubw_prefix_attn_workspace_bytes(
+        batch, groups, tokens, max_tree, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return torch.empty(-(-n.value // 4), dtype=torch.float32, device=device)
+
+
+def prefix_attn(q, cache, table, q_start, ctx_len, group_start, prefix_len, masks=None, *, max_tree, workspace, max_len=0,
+                scale=None, out=None, lse=None):
+    """tree_attn for sequences that have the beginning of their contexts in common: the sequences group_start[g] ..
+    group_start[g + 1] - 1 (int32 [groups + 1], ascending) hold the same keys and values at the first prefix_len[g]
+    (int32 [groups]) positions, which are read once for all of them, by the table row of the first sequence that has
+    tokens. Sequences in no group have their contexts for themselves. workspace: prefix_attn_workspace(); the other
+    arguments as tree_attn's."""
+    out, first, last = _attn_args(q, cache, table, q_start, ctx_len, masks, scale, out, lse)
+    i32, dev = torch.int32, cache.index
+    groups = prefix_len.numel()
+    _launch("ubw_prefix_attn", dev, *first, _flat(group_start, "group_start", i32, dev, groups + 1),
+            _flat(prefix_len, "prefix_len", i32, dev), groups, max_tree, max_len, *last, *_scratch(workspace, dev))
     return out
 
 

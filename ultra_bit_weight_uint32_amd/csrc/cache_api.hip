@@ -30,6 +30,58 @@ int check_table(const int32_t* table, int64_t ld, int cols) {
     return UBW_OK;
 }
 
+// What the attention calls check alike, and the arguments they share. UBW_OK with a.tokens == 0: nothing to do.
+int attn_args(AttnArgs* to, const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+              const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table, int table_cols,
+              int max_tree, const uint64_t* masks, float scale, void* out, int64_t ldo, float* lse, int* head_dim) {
+    if (!cache || tokens < 0 || batch < 0 || heads < 1 || max_tree < 1) return UBW_EINVAL;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return UBW_EINVAL;
+    const ubw_kv_cache c = with_used_strides(*cache);
+    int st = check_cache(&c);
+    if (st != UBW_OK) return st;
+    *head_dim = c.head_dim;
+    if (heads % c.kv_heads != 0) return UBW_EINVAL;
+    if (!half_type(q_dtype) || (c.dtype != UBW_E4M3 && c.dtype != q_dtype)) return UBW_EUNSUPPORTED;
+    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536 || heads / c.kv_heads > 1024)
+        return UBW_ERANGE;
+    if (tokens == 0 || batch == 0) return UBW_OK;
+    if (!q_start || !ctx_len) return UBW_EINVAL;
+    if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
+    if ((int64_t)table_cols * c.page_size > (1 << 30)) return UBW_ERANGE;  // positions stay clear of 2^31
+    if ((st = check_rows(q, ldq, tokens, heads, c.head_dim, 2)) != UBW_OK ||
+        (st = check_rows(out, ldo, tokens, heads, c.head_dim, 2)) != UBW_OK)
+        return st;
+    if ((reinterpret_cast<uintptr_t>(masks) & 7) || !aligned4(lse) || !aligned4(q_start) || !aligned4(ctx_len)) return UBW_EALIGN;
+    AttnArgs a{};
+    a.c = pages_of(c);
+    a.q = q;
+    a.out = out;
+    a.ldq = ldq;
+    a.ldo = ldo;
+    a.tokens = (int)tokens;
+    a.heads = heads;
+    a.group = heads / c.kv_heads;
+    a.batch = batch;
+    a.q_start = q_start;
+    a.ctx_len = ctx_len;
+    a.table = table;
+    a.ld_table = ld_table;
+    a.table_cols = table_cols;
+    a.max_tree = max_tree;
+    a.masks = masks;
+    a.scale = scale;
+    a.lse = lse;
+    *to = a;
+    return UBW_OK;
+}
+
+// Scratch of `need` bytes: NULL with 0 bytes where it may be left out.
+int check_workspace(const void* ws, size_t bytes, size_t need, bool may_lack) {
+    if (!ws) return may_lack && bytes == 0 ? UBW_OK : UBW_EINVAL;
+    if (!aligned16(ws)) return UBW_EALIGN;
+    return bytes < need ? UBW_ESIZE : UBW_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -95,56 +147,63 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
                   const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
                   int table_cols, int max_tree, int64_t max_len, const uint64_t* masks, float scale, void* out,
                   int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream) {
-    if (!cache || tokens < 0 || batch < 0 || heads < 1 || max_tree < 1 || max_len < 0) return UBW_EINVAL;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return UBW_EINVAL;
-    const ubw_kv_cache c = with_used_strides(*cache);
-    int st = check_cache(&c);
-    if (st != UBW_OK) return st;
-    if (heads % c.kv_heads != 0) return UBW_EINVAL;
-    if (!half_type(q_dtype) || (c.dtype != UBW_E4M3 && c.dtype != q_dtype)) return UBW_EUNSUPPORTED;
-    if (batch > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536 || heads / c.kv_heads > 1024)
-        return UBW_ERANGE;
-    if (tokens == 0 || batch == 0) return UBW_OK;
-    if (!q_start || !ctx_len) return UBW_EINVAL;
-    if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
-    if ((int64_t)table_cols * c.page_size > (1 << 30)) return UBW_ERANGE;  // positions stay clear of 2^31
-    if ((st = check_rows(q, ldq, tokens, heads, c.head_dim, 2)) != UBW_OK ||
-        (st = check_rows(out, ldo, tokens, heads, c.head_dim, 2)) != UBW_OK)
-        return st;
-    if ((reinterpret_cast<uintptr_t>(masks) & 7) || !aligned4(lse) || !aligned4(q_start) || !aligned4(ctx_len)) return UBW_EALIGN;
-    size_t need = 0;
-    if ((st = ubw_tree_attn_workspace_bytes(batch, max_tree, heads, c.kv_heads, c.head_dim, &need)) != UBW_OK) return st;
-    if (!workspace && ws_bytes != 0) return UBW_EINVAL;
-    if (workspace && !aligned16(workspace)) return UBW_EALIGN;
-    if (workspace && ws_bytes < need) return UBW_ESIZE;
-    const int64_t rows = (int64_t)max_tree * (heads / c.kv_heads);
-    const AttnTile t = attn_tile(rows, c.head_dim);
-    if (attn_max_items(batch, rows, c.kv_heads, c.head_dim, t) > kMaxGrid) return UBW_ERANGE;
+    if (max_len < 0) return UBW_EINVAL;
     AttnArgs a{};
-    a.c = pages_of(c);
-    a.q = q;
-    a.out = out;
-    a.ldq = ldq;
-    a.ldo = ldo;
-    a.tokens = (int)tokens;
-    a.heads = heads;
-    a.group = heads / c.kv_heads;
-    a.batch = batch;
-    a.q_start = q_start;
-    a.ctx_len = ctx_len;
-    a.table = table;
-    a.ld_table = ld_table;
-    a.table_cols = table_cols;
-    a.max_tree = max_tree;
-    a.masks = masks;
-    a.scale = scale;
-    a.lse = lse;
+    int d = 0, st = attn_args(&a, cache, q, q_dtype, ldq, tokens, heads, q_start, ctx_len, batch, table, ld_table, table_cols,
+                              max_tree, masks, scale, out, ldo, lse, &d);
+    if (st != UBW_OK || a.tokens == 0) return st;
+    size_t need = 0;
+    if ((st = ubw_tree_attn_workspace_bytes(batch, max_tree, heads, a.c.heads, d, &need)) != UBW_OK ||
+        (st = check_workspace(workspace, ws_bytes, need, true)) != UBW_OK)
+        return st;
+    const int64_t rows = (int64_t)max_tree * a.group;
+    const AttnTile t = attn_tile(rows, d);
+    if (attn_max_items(batch, rows, a.c.heads, d, t) > kMaxGrid) return UBW_ERANGE;
     a.ws = static_cast<float*>(workspace);
-    a.max_items = attn_max_items(batch, rows, c.kv_heads, c.head_dim, t);
+    a.max_items = attn_max_items(batch, rows, a.c.heads, d, t);
     // short contexts (as the table or the caller says) are not split: one launch
-    const int64_t room = (int64_t)table_cols * c.page_size, longest = max_len > 0 && max_len < room ? max_len : room;
-    a.target = workspace && longest > attn_unsplit(t, c.head_dim, (int64_t)batch * c.kv_heads) ? attn_target(t, c.head_dim) : 0;
-    return hip_status(launch_attn(a, c.dtype, q_dtype, c.head_dim, t, as_stream(stream)));
+    const int64_t room = (int64_t)table_cols << a.c.lps, longest = max_len > 0 && max_len < room ? max_len : room;
+    a.target = workspace && longest > attn_unsplit(t, d, (int64_t)batch * a.c.heads) ? attn_target(t, d) : 0;
+    return hip_status(launch_attn(a, cache->dtype, q_dtype, d, t, as_stream(stream)));
+}
+
+int ubw_prefix_attn_workspace_bytes(int batch, int groups, int64_t tokens, int max_tree, int heads, int kv_heads,
+                                    int head_dim, size_t* out) {
+    if (!out || batch < 0 || groups < 0 || tokens < 0 || max_tree < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0)
+        return UBW_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return UBW_EUNSUPPORTED;
+    if (batch > UBW_MAX_SEQS || groups > UBW_MAX_SEQS || max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536 ||
+        kv_heads > 4096 || heads / kv_heads > 1024 || tokens * (heads / kv_heads) > (1 << 30))
+        return UBW_ERANGE;
+    *out = (size_t)prefix_workspace_floats(batch, groups, tokens, max_tree, heads / kv_heads, kv_heads, head_dim) * 4;
+    return UBW_OK;
+}
+
+int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+                    const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
+                    int table_cols, const int32_t* group_start, const int32_t* prefix_len, int groups, int max_tree,
+                    int64_t max_len, const uint64_t* masks, float scale, void* out, int64_t ldo, float* lse, void* workspace,
+                    size_t ws_bytes, void* stream) {
+    if (max_len < 0 || groups < 0) return UBW_EINVAL;
+    PrefixArgs a{};
+    int d = 0, st = attn_args(&a, cache, q, q_dtype, ldq, tokens, heads, q_start, ctx_len, batch, table, ld_table, table_cols,
+                              max_tree, masks, scale, out, ldo, lse, &d);
+    if (st != UBW_OK || a.tokens == 0) return st;
+    if (groups > 0 && (!group_start || !prefix_len)) return UBW_EINVAL;
+    if (!aligned4(group_start) || !aligned4(prefix_len)) return UBW_EALIGN;
+    size_t need = 0;
+    if ((st = ubw_prefix_attn_workspace_bytes(batch, groups, tokens, max_tree, heads, a.c.heads, d, &need)) != UBW_OK ||
+        (st = check_workspace(workspace, ws_bytes, need, false)) != UBW_OK)
+        return st;
+    a.z = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * a.group, a.group, a.c.heads, d);
+    if (a.z.cap_shared > kMaxGrid || a.z.cap_own > kMaxGrid) return UBW_ERANGE;
+    a.group_start = group_start;
+    a.prefix_len = prefix_len;
+    a.groups = groups;
+    a.ws = static_cast<float*>(workspace);
+    a.own_at = a.z.cap_shared * a.z.rb_shared * (d + 2);
+    a.plan = reinterpret_cast<int*>(a.ws + prefix_floats(a.z, d));
+    return hip_status(launch_prefix_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
 }
 
 int ubw_cache_copy_pages(const ubw_kv_cache* cache, const int32_t* pairs, int64_t count, void* stream) {

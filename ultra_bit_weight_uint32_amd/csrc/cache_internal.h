@@ -73,6 +73,15 @@ struct AttnArgs {
 };
 hipError_t launch_attn(const AttnArgs& a, int cache_dtype, int q_dtype, int head_dim, AttnTile t, hipStream_t s);
 
+struct PrefixArgs : AttnArgs {
+    const int32_t *group_start, *prefix_len;
+    int groups;
+    int* plan;        // behind the sums
+    int64_t own_at;   // floats before the sums of the pieces behind the prefixes
+    PrefixSizes z;
+};
+hipError_t launch_prefix_attn(const PrefixArgs& a, int cache_dtype, int q_dtype, int head_dim, hipStream_t s);
+
 hipError_t launch_copy_pages(const Pages& c, int layers, int page_size, int row_bytes, const int32_t* pairs, int count,
                              hipStream_t s);
 hipError_t launch_compact(const Pages& c, int layers, int row_bytes, const int32_t* table, int64_t ld_table,

@@ -170,5 +170,43 @@ inline int64_t attn_workspace_floats(int batch, int max_tree, int group, int kv_
     return most + batch + 1;
 }
 
+// ---- attention over shared prefixes ---------------------------------------------------------
+// Two lists of pieces: of each group's prefix, with blocks of its tokens' rows, and of what each sequence has
+// behind it. Blocks of 128 rows (64 of 256 dims) for prefixes; for the rest 16 where a sequence has no more.
+inline AttnTile prefix_tile(int head_dim) { return AttnTile{head_dim == 256 ? 1 : 2, 4}; }
+inline AttnTile own_tile(int64_t max_rows, int head_dim) { return max_rows <= 16 ? AttnTile{1, 1} : prefix_tile(head_dim); }
+struct PrefixSizes {
+    int rb_shared, rb_own;          // rows of a block
+    int target_shared, target_own;  // pieces aimed at
+    int64_t blocks_shared;          // most blocks of rows of all groups and heads
+    int64_t cap_shared, cap_own;    // most pieces
+};
+inline PrefixSizes prefix_sizes(int batch, int groups, int64_t tokens, int64_t max_rows, int group, int kv_heads, int head_dim) {
+    const AttnTile own = own_tile(max_rows, head_dim);
+    PrefixSizes p{};
+    p.rb_shared = attn_rows(prefix_tile(head_dim));
+    p.rb_own = attn_rows(own);
+    p.target_shared = attn_target(prefix_tile(head_dim), head_dim);
+    p.target_own = attn_target(own, head_dim);
+    p.blocks_shared = groups > 0 ? (tokens * group / p.rb_shared + groups) * kv_heads : 0;
+    p.cap_shared = groups > 0 ? p.target_shared + p.blocks_shared : 0;
+    p.cap_own = attn_max_items(batch, max_rows, kv_heads, head_dim, own);
+    return p;
+}
+// The plan, in 32-bit words: the lists' sizes, five words a group and four a sequence, and the ends of both lists.
+constexpr int kPlanHead = 8;
+inline int64_t prefix_plan_words(int batch, int groups) { return kPlanHead + 6 * ((int64_t)groups + 1) + 4 * ((int64_t)batch + 1); }
+inline int64_t prefix_floats(const PrefixSizes& p, int head_dim) {
+    return (p.cap_shared * p.rb_shared + p.cap_own * p.rb_own) * (head_dim + 2);
+}
+inline int64_t prefix_workspace_floats(int batch, int groups, int64_t tokens, int max_tree, int group, int kv_heads, int head_dim) {
+    int64_t most = 0;
+    for (int n = 1; n <= max_tree; ++n) {
+        const int64_t x = prefix_floats(prefix_sizes(batch, groups, tokens, (int64_t)n * group, group, kv_heads, head_dim), head_dim);
+        most = x > most ? x : most;
+    }
+    return most + prefix_plan_words(batch, groups);
+}
+
 }  // namespace cache
 }  // namespace ubw
