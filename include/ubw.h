@@ -558,6 +558,73 @@ int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64
                     size_t ws_bytes, void* stream);
 
 /*
+ * Attention over selected blocks of long contexts, in three calls. A block is a page; the whole blocks of a context of
+ * L positions are the table columns 0 .. L / page_size - 1.
+ *
+ * Bounds of keys: for pages that were filled when the sequences grew from start[b] to stop[b] positions (the columns
+ * start[b] / page_size .. stop[b] / page_size - 1 of table row b) the smallest and the largest element of every dim
+ * over the page's rows, in every layer; a NaN among them makes both NaN. Elements of 8 bits are compared as they are,
+ * without k_scale.
+ *   bounds   [layers][pages][kv_heads][2][head_dim] of the cache's type, contiguous, 16-byte aligned: [0] smallest,
+ *            [1] largest. Pages that are not named keep theirs; columns beyond table_cols or on a page outside
+ *            [0, pages) are skipped. Sequences that share a page write the same.
+ *   start, stop  int32 [batch] (below 0 counts as 0)
+ *   max_new  the largest stop[b] - start[b] (it only steers the launch); 0: unknown
+ * batch = 0 enqueues nothing.
+ * Errors: UBW_EINVAL, UBW_EUNSUPPORTED (as ubw_qk_norm_rope for the cache), UBW_ERANGE (batch above UBW_MAX_SEQS),
+ *         UBW_EALIGN, UBW_EHIP.
+ */
+int ubw_page_bounds(const ubw_kv_cache* cache, void* bounds, const int32_t* table, int64_t ld_table, int table_cols,
+                    const int32_t* start, const int32_t* stop, int batch, int64_t max_new, void* stream);
+
+/*
+ * The choice: for each token t and key/value head h, `count` whole blocks of its sequence's context. The score of a
+ * block with bounds lo, hi is
+ *   sum over h's query heads g and dims d of max(q[t][g][d] lo[d], q[t][g][d] hi[d]),
+ * summed in 64 bits: no sum over g of q[t][g] . k for a key k of the block is larger. The first `first` and the last
+ * `last` whole blocks are always chosen, then those of the largest scores (a NaN counts as the largest; equal ones:
+ * the lowest index first). Contexts of `count` whole blocks or fewer have all of them chosen.
+ *   bounds   of one layer, [pages][kv_heads][2][head_dim] of type dtype, as ubw_page_bounds leaves them. (k_scale, one
+ *            factor for all blocks of a head, does not change the choice.)
+ *   q        q_dtype (UBW_F16 or UBW_BF16; dtype unless that is UBW_E4M3), rows as in ubw_tree_attn
+ *   q_start, ctx_len, table, max_tree  as in ubw_tree_attn. A block on no valid page is chosen last.
+ *   max_len  the largest context (with or without the tokens behind it); 0: unknown. Blocks beyond it are not looked at.
+ *   blocks   OUT int32 [tokens][kv_heads][count], ascending block indices, then -1. Rows of tokens that belong to no
+ *            sequence (or lie behind a sequence's max_tree-th) are left as they were.
+ *   first + last <= count
+ *   workspace  ubw_block_select_workspace_bytes() bytes for max_blocks = table_cols, or max_len / page_size + 1 where
+ *            that is given and smaller; always needed, as the other workspaces without contents between calls.
+ * tokens = 0 or batch = 0 enqueues nothing.
+ * Errors: UBW_EINVAL (null, sizes, count < 1, first + last above count, heads no multiple of kv_heads),
+ *         UBW_EUNSUPPORTED (types, head_dim, page_size), UBW_ERANGE (as ubw_tree_attn; count above 2^20), UBW_EALIGN,
+ *         UBW_ESIZE (workspace), UBW_EHIP.
+ */
+int ubw_block_select_workspace_bytes(int64_t tokens, int kv_heads, int64_t max_blocks, size_t* out);
+int ubw_block_select(const void* bounds, int dtype, int pages, int page_size, int kv_heads, int head_dim, const void* q,
+                     int q_dtype, int64_t ldq, int64_t tokens, int heads, const int32_t* q_start, const int32_t* ctx_len,
+                     int batch, const int32_t* table, int64_t ld_table, int table_cols, int max_tree, int64_t max_len, int count,
+                     int first, int last, int32_t* blocks, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * ubw_tree_attn where a token sees, of the whole blocks of its sequence's context, only those of its list (one for
+ * each key/value head). The positions behind the whole blocks (the rest of the context, on the page where it ends)
+ * and the tokens of its tree are seen as there.
+ *   blocks   int32 [tokens][kv_heads][count], e.g. from ubw_block_select: ascending indices of whole blocks. A list
+ *            ends at its first entry that is below 0, not above the entry before it, or no whole block of the context
+ *            (within table_cols). count may be 0 (blocks then NULL).
+ *   workspace  ubw_block_attn_workspace_bytes() bytes for as many tokens or more, or NULL with 0 bytes: lists are then
+ *            not split over workgroups.
+ *   Everything else as ubw_tree_attn.
+ * tokens = 0 or batch = 0 enqueues nothing.
+ * Errors: as ubw_tree_attn; UBW_ERANGE (count above 2^20, count * page_size about 2^30).
+ */
+int ubw_block_attn_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim, size_t* out);
+int ubw_block_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+                   const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
+                   int table_cols, const int32_t* blocks, int count, int max_tree, const uint64_t* masks, float scale, void* out,
+                   int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Copies whole pages, keys and values of every layer: page pairs[i][0] to page pairs[i][1]. A pair
  * with an entry outside [0, pages) is skipped. No page may be the target of two pairs, or the
  * target of one and the source of another (its contents are then unspecified; nothing else is).

@@ -36,7 +36,9 @@ EXPORTS = (
     "ubw_lut_gemv_multi", "ubw_lut_gemv_gs", "ubw_fit_workspace_bytes", "ubw_fit_bases",
     "ubw_gram", "ubw_saliency_workspace_bytes", "ubw_hessian_saliency",
     "ubw_qk_norm_rope", "ubw_tree_attn_workspace_bytes", "ubw_tree_attn",
-    "ubw_prefix_attn_workspace_bytes", "ubw_prefix_attn", "ubw_cache_copy_pages",
+    "ubw_prefix_attn_workspace_bytes", "ubw_prefix_attn", "ubw_page_bounds",
+    "ubw_block_select_workspace_bytes", "ubw_block_select", "ubw_block_attn_workspace_bytes", "ubw_block_attn",
+    "ubw_cache_copy_pages",
     "ubw_cache_compact", "ubw_pages_init", "ubw_pages_trim", "ubw_pages_fork", "ubw_pages_reserve",
 )
 
@@ -121,6 +123,11 @@ def lib():
         "ubw_tree_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, I, I64, P, F, P, I64, P, P, SZ, P], I),
         "ubw_prefix_attn_workspace_bytes": ([I, I, I64, I, I, I, I, ctypes.POINTER(SZ)], I),
         "ubw_prefix_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, P, P, I, I, I64, P, F, P, I64, P, P, SZ, P], I),
+        "ubw_page_bounds": ([C, P, P, I64, I, P, P, I, I64, P], I),
+        "ubw_block_select_workspace_bytes": ([I64, I, I64, ctypes.POINTER(SZ)], I),
+        "ubw_block_select": ([P, I, I, I, I, I, P, I, I64, I64, I, P, P, I, P, I64, I, I, I64, I, I, I, P, P, SZ, P], I),
+        "ubw_block_attn_workspace_bytes": ([I64, I, I, I, ctypes.POINTER(SZ)], I),
+        "ubw_block_attn": ([C, P, I, I64, I64, I, P, P, I, P, I64, I, P, I, I, P, F, P, I64, P, P, SZ, P], I),
         "ubw_cache_copy_pages": ([C, P, I64, P], I),
         "ubw_cache_compact": ([C, P, I64, I, P, P, I, I, P], I),
         "ubw_pages_init": ([PP, P], I),
@@ -639,7 +646,7 @@ def bench_stream_read(buf, nbytes: int, out):
 # ---------------------------------------------------------------------------------------------
 # keys and values in a paged cache (cache.py, loaded with torch on first use)
 
-_CACHE_CALLS = ("KVCache", "PagePool", "cache_compact", "cache_copy_pages", "page_pool", "pages_fork", "pages_reserve",
+_CACHE_CALLS = ("KVCache", "PagePool", "block_attn", "block_attn_workspace", "block_select", "block_select_workspace", "cache_compact", "cache_copy_pages", "page_bounds", "page_pool", "pages_fork", "pages_reserve",
                 "pages_trim", "prefix_attn", "prefix_attn_workspace", "qk_norm_rope", "tree_attn", "tree_attn_workspace")
 
 

@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libubw.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kernels.hip", "rows4.hip", "mfma.hip", "fit.hip", "saliency.hip", "api.hip",
-                                                    "rope.hip", "attn.hip", "prefix.hip", "pages.hip", "cache_api.hip")]
+                                                    "rope.hip", "attn.hip", "prefix.hip", "blocks.hip", "select.hip", "pages.hip",
+                                                    "cache_api.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

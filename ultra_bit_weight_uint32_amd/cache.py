@@ -242,6 +242,80 @@ def prefix_attn(q, cache, table, q_start, ctx_len, group_start, prefix_len, mask
     return out
 
 
+def page_bounds(cache, bounds, table, start, stop, *, max_new=0):
+    """The smallest and the largest key element of every dim, for the pages that were filled when the sequences grew
+    from start to stop positions (int32 [batch] each): the columns start // page_size .. stop // page_size - 1 of
+    table, in every layer. bounds [layers, pages, kv_heads, 2, head_dim] (without layers where the cache has none), of
+    the cache's type, takes them at [..., 0, :] and [..., 1, :]; other pages' stay. max_new: the most positions a
+    sequence grew by (0: unknown)."""
+    dev, i32 = cache.index, torch.int32
+    shape = cache.k.shape[:-2] + (2, cache.head_dim)
+    batch = start.numel()
+    tp, ld_table, cols = _table(table, batch, dev)
+    _launch("ubw_page_bounds", dev, cache.ref, _flat(bounds, "bounds", cache.dtype, dev, shape=shape), tp, ld_table, cols,
+            _flat(start, "start", i32, dev), _flat(stop, "stop", i32, dev, batch), batch, max_new)
+
+
+def block_select_workspace(tokens, kv_heads, max_blocks, device="cuda"):
+    """Scratch for block_select calls of up to this many tokens over tables of up to max_blocks columns (reusable on one
+    stream)."""
+    n = ctypes.c_size_t()
+    _check("ubw_block_select_workspace_bytes",
+           lib().ubw_block_select_workspace_bytes(tokens, kv_heads, max_blocks, ctypes.byref(n)))
+    return torch.empty(-(-n.value // 8), dtype=torch.int64, device=device)
+
+
+def block_select(q, bounds, table, q_start, ctx_len, count, *, page_size, max_tree, workspace, first=1, last=1, max_len=0,
+                 out=None):
+    """For each token and key/value head the `count` whole blocks (pages) of its sequence's context that its query heads
+    may score highest, by the keys' bounds [pages, kv_heads, 2, head_dim] of one layer (page_bounds()); the `first`
+    and the `last` whole blocks are always among them. Returns out, int32 [tokens, kv_heads, count]: block indices
+    (columns of table), ascending, -1 behind them where the context has fewer. workspace: block_select_workspace();
+    the other arguments as tree_attn's."""
+    if not isinstance(bounds, _Tensor) or bounds.dim() != 4 or bounds.shape[2] != 2 or not bounds.is_cuda:
+        raise ValueError("bounds must be a GPU tensor [pages, kv_heads, 2, head_dim]")
+    dev, i32 = bounds.get_device(), torch.int32
+    pages, kv, _, dim = bounds.shape
+    dtype = bounds.dtype
+    if dtype not in _TYPES or dtype is torch.float32:
+        raise TypeError(f"bounds has dtype {dtype}, expected float16, bfloat16 or float8_e4m3fn")
+    qp, ldq, t, heads = _rows(q, "q", dev, dim)
+    if q.dtype is not torch.float16 and q.dtype is not torch.bfloat16:
+        raise TypeError(f"q has dtype {q.dtype}, expected float16 or bfloat16")
+    batch = ctx_len.numel()
+    tp, ld_table, cols = _table(table, batch, dev)
+    if out is None:
+        out = torch.empty((t, kv, max(count, 0)), dtype=i32, device=bounds.device)
+    _launch("ubw_block_select", dev, _flat(bounds, "bounds", dtype, dev), _TYPES[dtype], pages, page_size, kv, dim, qp,
+            _TYPES[q.dtype], ldq, t, heads, _flat(q_start, "q_start", i32, dev, batch + 1), _flat(ctx_len, "ctx_len", i32, dev),
+            batch, tp, ld_table, cols, max_tree, max_len, count, first, last,
+            _flat(out, "out", i32, dev, shape=(t, kv, count)), *_scratch(workspace, dev))
+    return out
+
+
+def block_attn_workspace(tokens, heads, kv_heads, head_dim, device="cuda"):
+    """Scratch for block_attn calls of up to this many tokens (reusable on one stream)."""
+    n = ctypes.c_size_t()
+    _check("ubw_block_attn_workspace_bytes",
+           lib().ubw_block_attn_workspace_bytes(tokens, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return torch.empty(-(-n.value // 4), dtype=torch.float32, device=device)
+
+
+def block_attn(q, cache, table, q_start, ctx_len, blocks, masks=None, *, max_tree, scale=None, out=None, lse=None,
+               workspace=None):
+    """tree_attn where a token sees, of its sequence's whole blocks (pages), only those in its list: blocks int32
+    [tokens, kv_heads, count], ascending block indices, as block_select() gives them; a list ends at its first entry that
+    does not ascend or is no whole block of the context. The page on which the context ends and the tokens behind it
+    are seen as in tree_attn. workspace: block_attn_workspace() (None: lists are not split over workgroups)."""
+    out, head, rest = _attn_args(q, cache, table, q_start, ctx_len, masks, scale, out, lse)
+    dev = cache.index
+    bp = _flat(blocks, "blocks", torch.int32, dev)
+    if blocks.dim() != 3 or blocks.shape[0] != q.shape[0] or blocks.shape[1] != cache.kv_heads:
+        raise ValueError(f"blocks must be [{q.shape[0]}, {cache.kv_heads}, count], got {list(blocks.shape)}")
+    _launch("ubw_block_attn", dev, *head, bp, blocks.shape[2], max_tree, *rest, *_scratch(workspace, dev))
+    return out
+
+
 def cache_copy_pages(cache, pairs):
     """Page pairs[i, 0] copied to page pairs[i, 1] (int32 [count, 2]), keys and values of every layer.
     Pairs with an entry outside the cache's pages, as (-1, -1), are skipped."""

@@ -139,6 +139,21 @@ __device__ inline int positions(const AttnArgs& a, const Seq& s) {
     const int64_t most = (int64_t)a.table_cols << a.c.lps;
     return (int)min((int64_t)s.ctx + s.n, most);
 }
+__device__ inline int units_of(int n) { return (int)(((int64_t)n + kAttnUnit - 1) / kAttnUnit); }
+// The last i with list[i] <= x, list ascending and list[0] <= x; 64 of them a step.
+__device__ inline int find_last(const int* list, int n, int x) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, span = n;
+    while (span > 1) {
+        const int step = (span + 63) >> 6;
+        const uint64_t b = __ballot(lane * step < span && list[lo + min(lane * step, span - 1)] <= x);
+        const int k = b ? 63 - __builtin_clzll(b) : 0;
+        lo += k * step;
+        span = min(step, span - k * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // Which of the four positions behind ctx + d (d may be negative: context, all seen) a token with this
 // mask sees. No branches: bit x of (mask << 4 | 15) is position ctx + x - 4.
 __device__ inline uint32_t four_seen(uint64_t mask, int d) {

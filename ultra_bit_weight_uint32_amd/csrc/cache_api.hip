@@ -206,6 +206,126 @@ int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64
     return hip_status(launch_prefix_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
 }
 
+int ubw_page_bounds(const ubw_kv_cache* cache, void* bounds, const int32_t* table, int64_t ld_table, int table_cols,
+                    const int32_t* start, const int32_t* stop, int batch, int64_t max_new, void* stream) {
+    if (!cache || batch < 0 || max_new < 0) return UBW_EINVAL;
+    const ubw_kv_cache c = with_used_strides(*cache);
+    int st = check_cache(&c);
+    if (st != UBW_OK) return st;
+    if (batch > UBW_MAX_SEQS) return UBW_ERANGE;
+    if (batch == 0) return UBW_OK;
+    if (!bounds || !start || !stop) return UBW_EINVAL;
+    if ((st = check_table(table, ld_table, table_cols)) != UBW_OK) return st;
+    if (!aligned16(bounds) || !aligned4(start) || !aligned4(stop)) return UBW_EALIGN;
+    BoundsArgs a{};
+    a.c = pages_of(c);
+    a.bounds = bounds;
+    a.table = table;
+    a.start = start;
+    a.stop = stop;
+    a.ld_table = ld_table;
+    a.table_cols = table_cols;
+    a.batch = batch;
+    a.layers = c.layers;
+    // pages that max_new positions fill at most
+    const int64_t pages = max_new > 0 && cdiv(max_new, c.page_size) < table_cols ? cdiv(max_new, c.page_size) : table_cols;
+    return hip_status(launch_page_bounds(a, c.dtype, c.head_dim, pages, as_stream(stream)));
+}
+
+int ubw_block_select_workspace_bytes(int64_t tokens, int kv_heads, int64_t max_blocks, size_t* out) {
+    if (!out || tokens < 0 || kv_heads < 1 || max_blocks < 1) return UBW_EINVAL;
+    if (tokens > (1 << 24) || kv_heads > 4096 || max_blocks > (1 << 24)) return UBW_ERANGE;
+    *out = (size_t)tokens * kv_heads * max_blocks * 8;
+    return UBW_OK;
+}
+
+int ubw_block_select(const void* bounds, int dtype, int pages, int page_size, int kv_heads, int head_dim, const void* q,
+                     int q_dtype, int64_t ldq, int64_t tokens, int heads, const int32_t* q_start, const int32_t* ctx_len,
+                     int batch, const int32_t* table, int64_t ld_table, int table_cols, int max_tree, int64_t max_len, int count,
+                     int first, int last, int32_t* blocks, void* workspace, size_t ws_bytes, void* stream) {
+    if (pages < 1 || kv_heads < 1 || tokens < 0 || heads < 1 || batch < 0 || max_tree < 1 || max_len < 0 || count < 1 || first < 0 ||
+        last < 0 || first > count - last || heads % kv_heads != 0)
+        return UBW_EINVAL;
+    if (dtype != UBW_F16 && dtype != UBW_BF16 && dtype != UBW_E4M3) return UBW_EUNSUPPORTED;
+    if (!half_type(q_dtype) || (dtype != UBW_E4M3 && dtype != q_dtype)) return UBW_EUNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return UBW_EUNSUPPORTED;
+    if (!page_size_ok(page_size)) return UBW_EUNSUPPORTED;
+    if (pages > (1 << 24) || (int64_t)pages * page_size > 0x7fffffff || kv_heads > 4096 || batch > UBW_MAX_SEQS ||
+        max_tree > UBW_MAX_TREE || tokens > (1 << 24) || heads > 65536 || heads / kv_heads > 1024 || count > (1 << 20))
+        return UBW_ERANGE;
+    if (tokens == 0 || batch == 0) return UBW_OK;
+    if (!bounds || !q_start || !ctx_len || !blocks) return UBW_EINVAL;
+    int st = check_table(table, ld_table, table_cols);
+    if (st != UBW_OK || (st = check_rows(q, ldq, tokens, heads, head_dim, 2)) != UBW_OK) return st;
+    if ((int64_t)table_cols * page_size > (1 << 30)) return UBW_ERANGE;
+    if (!aligned16(bounds) || !aligned4(q_start) || !aligned4(ctx_len) || !aligned4(blocks)) return UBW_EALIGN;
+    // blocks there can be
+    const int64_t most = max_len > 0 && max_len / page_size + 1 < table_cols ? max_len / page_size + 1 : table_cols;
+    size_t need = 0;
+    if ((st = ubw_block_select_workspace_bytes(tokens, kv_heads, most, &need)) != UBW_OK ||
+        (st = check_workspace(workspace, ws_bytes, need, false)) != UBW_OK)
+        return st;
+    if (select_grid(kv_heads, most, max_tree) > kMaxGrid) return UBW_ERANGE;
+    SelectArgs a{};
+    a.bounds = bounds;
+    a.q = q;
+    a.ldq = ldq;
+    a.tokens = (int)tokens;
+    a.heads = heads;
+    a.group = heads / kv_heads;
+    a.kv = kv_heads;
+    a.batch = batch;
+    a.pages = pages;
+    a.lps = log2_of(page_size);
+    a.q_start = q_start;
+    a.ctx_len = ctx_len;
+    a.table = table;
+    a.ld_table = ld_table;
+    a.table_cols = table_cols;
+    a.max_tree = max_tree;
+    a.count = count;
+    a.first = first;
+    a.last = last;
+    a.blocks = blocks;
+    a.keys = static_cast<uint64_t*>(workspace);
+    a.stride = (int)most;
+    return hip_status(launch_block_select(a, dtype, q_dtype, head_dim, as_stream(stream)));
+}
+
+int ubw_block_attn_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim, size_t* out) {
+    if (!out || tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0) return UBW_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return UBW_EUNSUPPORTED;
+    if (tokens > (1 << 24) || heads > 65536 || kv_heads > 4096 || heads / kv_heads > 1024) return UBW_ERANGE;
+    *out = (size_t)block_workspace_floats(tokens, heads / kv_heads, kv_heads, head_dim) * 4;
+    return UBW_OK;
+}
+
+int ubw_block_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
+                   const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
+                   int table_cols, const int32_t* blocks, int count, int max_tree, const uint64_t* masks, float scale, void* out,
+                   int64_t ldo, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    if (count < 0) return UBW_EINVAL;
+    BlockArgs a{};
+    int d = 0, st = attn_args(&a, cache, q, q_dtype, ldq, tokens, heads, q_start, ctx_len, batch, table, ld_table, table_cols,
+                              max_tree, masks, scale, out, ldo, lse, &d);
+    if (st != UBW_OK || a.tokens == 0) return st;
+    if (count > 0 && !blocks) return UBW_EINVAL;
+    if (!aligned4(blocks)) return UBW_EALIGN;
+    if (count > (1 << 20) || block_positions(count, cache->page_size, max_tree) > (1 << 30)) return UBW_ERANGE;
+    size_t need = 0;
+    if ((st = ubw_block_attn_workspace_bytes(tokens, heads, a.c.heads, d, &need)) != UBW_OK ||
+        (st = check_workspace(workspace, ws_bytes, need, true)) != UBW_OK)
+        return st;
+    const int64_t pairs = block_pairs(tokens, a.group, a.c.heads, block_tile(a.group, d));
+    a.splits = workspace ? block_splits(pairs, block_positions(count, cache->page_size, max_tree)) : 1;
+    if (block_cap(pairs) > kMaxGrid) return UBW_ERANGE;
+    a.blocks = blocks;
+    a.count = count;
+    a.ws = static_cast<float*>(workspace);
+    a.cut = workspace ? reinterpret_cast<int*>(a.ws + block_floats(tokens, a.group, a.c.heads, d)) : nullptr;
+    return hip_status(launch_block_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
+}
+
 int ubw_cache_copy_pages(const ubw_kv_cache* cache, const int32_t* pairs, int64_t count, void* stream) {
     if (!cache || count < 0) return UBW_EINVAL;
     const ubw_kv_cache c = with_used_strides(*cache);

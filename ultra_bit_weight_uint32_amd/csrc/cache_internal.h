@@ -82,6 +82,35 @@ struct PrefixArgs : AttnArgs {
 };
 hipError_t launch_prefix_attn(const PrefixArgs& a, int cache_dtype, int q_dtype, int head_dim, hipStream_t s);
 
+struct BlockArgs : AttnArgs {
+    const int32_t* blocks;
+    int count, splits;
+    int* cut;  // [heads][tokens] pieces that a row's positions are cut into (splits > 1)
+};
+hipError_t launch_block_attn(const BlockArgs& a, int cache_dtype, int q_dtype, int head_dim, hipStream_t s);
+
+struct BoundsArgs {
+    Pages c;
+    void* bounds;
+    const int32_t *table, *start, *stop;
+    int64_t ld_table;
+    int table_cols, batch, layers;
+};
+hipError_t launch_page_bounds(const BoundsArgs& a, int dtype, int head_dim, int64_t pages, hipStream_t s);
+
+struct SelectArgs {
+    const void *bounds, *q;
+    int64_t ldq;
+    int tokens, heads, group, kv, batch, pages, lps;
+    const int32_t *q_start, *ctx_len, *table;
+    int64_t ld_table;
+    int table_cols, max_tree, count, first, last;
+    int32_t* blocks;
+    uint64_t* keys;  // [tokens][kv][stride]
+    int stride;
+};
+hipError_t launch_block_select(const SelectArgs& a, int dtype, int q_dtype, int head_dim, hipStream_t s);
+
 hipError_t launch_copy_pages(const Pages& c, int layers, int page_size, int row_bytes, const int32_t* pairs, int count,
                              hipStream_t s);
 hipError_t launch_compact(const Pages& c, int layers, int row_bytes, const int32_t* table, int64_t ld_table,

@@ -208,5 +208,39 @@ inline int64_t prefix_workspace_floats(int batch, int groups, int64_t tokens, in
     return most + prefix_plan_words(batch, groups);
 }
 
+// ---- selected blocks ------------------------------------------------------------------------
+// Attention over them: a token and key/value head have their rows (the head's queries) and positions to
+// themselves. Their number is bounded by the list's length, which the host knows, and so is the cut.
+inline int64_t block_positions(int count, int page_size, int max_tree) { return (int64_t)count * page_size + page_size - 1 + max_tree; }
+inline AttnTile block_tile(int group, int head_dim) { return own_tile(group, head_dim); }
+inline int64_t block_pairs(int64_t tokens, int group, int kv_heads, AttnTile t) { return tokens * kv_heads * cdiv(group, attn_rows(t)); }
+constexpr int kBlockTarget = 512;  // pieces aimed at
+inline int block_splits(int64_t pairs, int64_t positions) {
+    const int64_t units = cdiv(positions, kAttnUnit), want = pairs > 0 ? cdiv(kBlockTarget, pairs) : 1;
+    return (int)(want < units ? want : units);
+}
+inline int64_t block_cap(int64_t pairs) { return kBlockTarget + pairs; }
+inline int64_t block_floats(int64_t tokens, int group, int kv_heads, int head_dim) {
+    const AttnTile t = block_tile(group, head_dim);
+    return block_cap(block_pairs(tokens, group, kv_heads, t)) * attn_rows(t) * (head_dim + 2);
+}
+inline int64_t block_workspace_floats(int64_t tokens, int group, int kv_heads, int head_dim) {
+    return block_floats(tokens, group, kv_heads, head_dim) + tokens * kv_heads;
+}
+
+// Bounds of pages: a group of lanes takes one page of one head in one layer. Groups for each sequence: as many as
+// its pages ask for, as far as the card holds them (each then takes several in turn).
+inline int64_t bounds_groups(int64_t layers, int kv_heads, int batch, int64_t pages) {
+    const int64_t all = layers * kv_heads * pages, most = cdiv((int64_t)1 << 18, batch);
+    return all < most ? all : most;
+}
+
+// Scores of blocks: blocks of one sequence and head that a workgroup takes.
+constexpr int kScoreBlocks = 64, kScoreBlocksTree = 256;
+inline int64_t select_grid(int kv_heads, int64_t blocks, int max_tree) {
+    const int64_t scores = cdiv(blocks, max_tree == 1 ? kScoreBlocks : kScoreBlocksTree) * kv_heads, rows = (int64_t)max_tree * kv_heads;
+    return scores > rows ? scores : rows;
+}
+
 }  // namespace cache
 }  // namespace ubw

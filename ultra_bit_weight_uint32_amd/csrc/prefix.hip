@@ -87,8 +87,6 @@ __device__ inline Two plan_before(Two mine, int64_t (&lds)[2][kPlanThreads / 64]
     }
     return s;
 }
-__device__ inline int units_of(int n) { return (int)(((int64_t)n + kAttnUnit - 1) / kAttnUnit); }
-
 // A thread has the groups and the sequences kEach t .. kEach t + kEach - 1.
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, bool one_row_wave) {
     __shared__ int start[kMost + 1], len[kMost], lead[kMost], last[kMost];
@@ -209,20 +207,6 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, bool one_ro
         at.head[0] = first;
         at.head[1] = own;
     }
-}
-
-// The last i with list[i] <= x, list ascending and list[0] <= x; 64 of them a step.
-__device__ inline int find_last(const int* list, int n, int x) {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, span = n;
-    while (span > 1) {
-        const int step = (span + 63) >> 6;
-        const uint64_t b = __ballot(lane * step < span && list[lo + min(lane * step, span - 1)] <= x);
-        const int k = b ? 63 - __builtin_clzll(b) : 0;
-        lo += k * step;
-        span = min(step, span - k * step);
-    }
-    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // PART: 1 the prefixes, 2 what is behind them.
