@@ -112,7 +112,9 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         items = a.batch * a.c.heads * blocks_max;
     }
 
-    attn_pieces<kTrees, TQ, FP8, D, MT, R, T, NS, NB, ONCE>(a, sh, items, a.ws, [&](int item, Piece& p) {
+    attn_pieces<kTrees, TQ, FP8, D, MT, R, T, NS, NB, ONCE>(a, sh, blockIdx.x, a.ws, [&](int it) { return it < 8 * xcd_share(items); }, [&](int it) { return it + (int)gridDim.x; }, [&](int it, Piece& p) {
+        const int item = xcd_item(it, items);
+        if (item >= items) return false;
         int b, split;
         Seq s;
         Plan n;
@@ -126,23 +128,23 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
             s = seq_at(a, b);
             n = plan_of(a, s, RB, chunk);
             int r = item - __builtin_amdgcn_readfirstlane(pre[b]);
-            p.blk = r % n.blocks;
+            p.r0 = r % n.blocks * RB;
             r /= n.blocks;
             split = r % n.splits;
             p.h = r / n.splits;
         } else {
-            p.blk = item % blocks_max;
+            p.r0 = item % blocks_max * RB;
             const int r = item / blocks_max;
             p.h = r % a.c.heads;
             b = r / a.c.heads;
             s = seq_at(a, b);
             n = plan_of(a, s, RB, 0);
             split = 0;
-            if (p.blk >= n.blocks) return false;
+            if (item % blocks_max >= n.blocks) return false;
         }
         attn_range(n.units, n.splits, split, &p.u0, &p.u1);
         p.row = b;
-        p.splits = n.splits;
+        p.slot = item;
         p.q0 = s.q0;
         p.rows = s.n * a.group;
         p.tree = p.base = 0;

@@ -37,6 +37,8 @@
 // of the build (packed fp32 off), so no scratch access is among the loop's loads either.
 // attn.hip, prefix.hip and blocks.hip say what their pieces are.
 #pragma once
+#include <type_traits>
+
 #include "cache_internal.h"
 
 namespace ubw {
@@ -141,7 +143,8 @@ __device__ inline int positions(const AttnArgs& a, const Seq& s) {
 }
 __device__ inline int units_of(int n) { return (int)(((int64_t)n + kAttnUnit - 1) / kAttnUnit); }
 // The last i with list[i] <= x, list ascending and list[0] <= x; 64 of them a step.
-__device__ inline int find_last(const int* list, int n, int x) {
+template <typename I>
+__device__ inline int find_last(const I* list, int n, I x) {
     const int lane = threadIdx.x & 63;
     int lo = 0, span = n;
     while (span > 1) {
@@ -191,12 +194,20 @@ struct Layout {
 // bytes (keys and values under one row block), they need not stay in the L2 (1.3 GB in 64 ragged sequences:
 // 229 us, 249 without; 0.85 GB under one block of 128 rows 161, 169 without; under four row blocks they are
 // read again: 638 us without, 648 with).
-template <bool ONCE>
-__device__ inline void to_lds(Rsrc r, uint32_t off, uint32_t lds) {
+template <bool ONCE, int MORE = 0>
+__device__ inline void to_lds(Rsrc r, uint32_t off, uint32_t lds) {  // MORE: added to the offset (and to m0)
+    lds -= MORE;
     if constexpr (ONCE)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 nt lds" ::"s"(lds), "v"(off), "s"(r), "n"(MORE) : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r) : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen offset:%3 lds" ::"s"(lds), "v"(off), "s"(r), "n"(MORE) : "memory");
+}
+template <int I, int N, typename F>
+__device__ __forceinline__ void each_of(const F& f) {  // f(I), .., f(N - 1), as constants
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each_of<I + 1, N>(f);
+    }
 }
 template <int N>
 __device__ inline void wait_loads() {  // all but the newest N transfers have arrived
@@ -297,23 +308,29 @@ struct Cfg {
 // pieces are, and in the page of a position.
 enum Mode {
     kTrees,   // tree attention: a sequence's tokens over its context and one another
-    kShared,  // a group's tokens over its prefix, read from the table row of its first sequence
-    kOwn,     // a sequence's tokens over what is behind its group's prefix
+    kParts,   // a group's tokens over its prefix (no tree), or a sequence's over what is behind it
     kBlocks,  // a token over the blocks of its list, the page where the context ends and its tree
 };
 struct Piece {
-    int h, blk;          // key/value head, block of rows
+    int h;               // key/value head
     int row;             // row of the table
-    int u0, u1, splits;  // units of positions; pieces that the rows' positions are cut into
-    int q0, rows, tree;  // first token, rows, place of the first token in its tree
+    int u0, u1;          // units of positions
+    int q0, rows, tree;  // first token, rows, place of the first token in its tree (kParts: -1, there is none)
+    int r0;              // first row of the block
     int base;            // position where unit 0 begins (a multiple of 16)
     int ctx, len;        // end of the context, of the positions
     int chosen, whole;   // kBlocks: blocks of the list, whole blocks of the context
     const int32_t* list;
+    int slot;            // its place in the workspace (kParts: -1, the rows' own)
     bool last;           // no other piece has these rows: they are done
 };
 // Workspace: pieces' rows of D means, then (m, l) of each row.
 __device__ inline float* piece_rows(float* ws, int item, int rb, int d) { return ws + (int64_t)item * rb * (d + 2); }
+
+// Workgroups go to the eight XCDs in turn; each XCD takes a contiguous eighth of the pieces, so that the row blocks
+// over the same keys and values, neighbours in the list, meet in one L2. i counts to 8 xcd_share(items).
+__device__ inline int xcd_share(int items) { return (items + 7) >> 3; }
+__device__ inline int xcd_item(int i, int items) { return (i & 7) * xcd_share(items) + (i >> 3); }
 
 // What a workgroup shares. odd: of each wave, it met values of the tree that are not finite in this piece. A
 // wave clears and sets its own word only, so both come in its own order; the others read it behind a barrier of
@@ -327,11 +344,13 @@ struct Shared {
     int beyond[C::kRowWaves * C::kPosWaves];
 };
 
-// Goes through this workgroup's share of `items` pieces; piece_of(item, piece) says what a piece is (false: nothing),
-// ws takes the sums of those that are not a row's only ones.
-template <Mode MODE, typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE, typename Args, typename PieceOf>
-__device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT, R, T, NS, NB>>& sh, int items, float* ws,
-                                            const PieceOf& piece_of) {
+// Goes through the pieces `it`, next(it), .. as long as more(it); piece_of(it, piece) says what a piece is (false:
+// nothing), ws takes the sums of those that are not a row's only ones (kParts: a row's at row_of(piece, row of the
+// block, token, query head)). Returns the `it` that ended it.
+template <Mode MODE, typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, bool ONCE, typename Args, typename More,
+          typename Next, typename PieceOf, typename RowOf = int>
+__device__ __forceinline__ int attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT, R, T, NS, NB>>& sh, int it, float* ws,
+                                           const More& more, const Next& next, const PieceOf& piece_of, const RowOf& row_of = 0) {
     using H = Half<TQ>;
     using L = Layout<FP8, D>;
     using C = Cfg<FP8, D, MT, R, T, NS, NB>;
@@ -366,7 +385,7 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
     const int rw = wave % R, tw = wave / R;
 
     const auto mask_of = [&](const Piece& p, int t) -> uint64_t {  // of token t of the piece
-        if constexpr (MODE == kShared) return 0;  // has no tree
+        if (MODE == kParts && p.tree < 0) return 0;
         return a.masks ? a.masks[p.q0 + t] : (2ull << (p.tree + t)) - 1;
     };
 
@@ -374,23 +393,24 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
     const uint32_t tile0 = buf0 + tw * (NB * NS * L::kBytes);
     const uint32_t koff = c * a.c.k_row + j * 16;
     const int vt = lane / L::P, vp = lane % L::P;           // row and column of a value piece
+    constexpr int VS = R == 1 ? 16 / L::RP : 1;             // value pieces of 16 rows
+    uint32_t voff[VS];
+#pragma unroll
+    for (int i = 0; i < VS; ++i) voff[i] = (uint32_t)(i * L::RP + vt) * a.c.v_row + (uint32_t)((vp ^ L::mix((i * L::RP + vt) & 15)) * 16);
     const int q4 = c >> 2, q2 = c >> 1;                     // a transposing read: rows by fours, by eights
     const int vrow = FP8 ? 4 * j + (q2 & 3) + (q2 & 4) * 4 : 4 * j + q4;
     const uint32_t vread = L::CK * 1024 + vrow * L::kRowB +
                            (FP8 ? L::mix(vrow) * 16 + (c & 1) * 8
                                 : (((c >> 1) & 1) ^ (L::mix(vrow) & 1)) * 16 + (c & 1) * 8 + (L::mix(vrow) & ~1) * 16);
 
-    // Workgroups go to the eight XCDs in turn; each XCD takes a contiguous eighth of the pieces, so that
-    // the row blocks over the same keys and values, neighbours in the list, meet in one L2.
-    const int eighth = (items + 7) >> 3;
-    for (int it = blockIdx.x; it < 8 * eighth; it += gridDim.x) {
-        const int item = (it & 7) * eighth + (it >> 3);
-        if (item >= items) continue;
+    for (; more(it); it = again ? it : next(it)) {
         Piece p;
-        if (!piece_of(item, p)) continue;
+        if (!piece_of(it, p)) continue;
         if (lane == 0) odd[wave] = 0;
         const int h = p.h, rows = p.rows, begin = p.base + p.u0 * U;
-        const int r0 = p.blk * RB + rw * 16 * MT + c;  // this lane's row of tile 0
+        const int r0 = p.r0 + rw * 16 * MT + c;  // this lane's row of tile 0
+        // a wave without rows only takes part in the transfers
+        const bool idle = MODE != kTrees && R > 1 && p.r0 + rw * 16 * MT >= rows;
 
         const char* kb = a.c.k + h * a.c.k_head;
         const char* vb = a.c.v + h * a.c.v_head;
@@ -432,6 +452,30 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
         // The transfers of this wave for the step at t, those from first to last of each tile; rows behind the
         // end or on no page arrive as zeros.
         const auto fetch = [&](int t, const Pg& pg, uint32_t at, int first, int last) {
+            if constexpr (R == 1) {
+                // One descriptor for the keys and one for the values of 16 positions: building one takes a dozen scalar
+                // instructions, as many as a SIMD of eight waves can issue in 50 cycles.
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) {
+                    const int x = t + 16 * sub, rows = pg.p[sub] < 0 ? 0 : min(16, t_end - x);
+                    const int64_t page = max(pg.p[sub], 0), row = x & pmask;
+                    if (sub * L::KL < last && (sub + 1) * L::KL > first) {
+                        const Rsrc r = rows16(kb + page * a.c.k_page + row * a.c.k_row, rows * a.c.k_row);
+                        each_of<0, L::KL>([&](auto piece) {
+                            const int i = sub * L::KL + piece.value;
+                            if (i >= first && i < last) to_lds<ONCE, piece.value * 64>(r, koff, at + i * 1024);
+                        });
+                    }
+                    if (L::CK + sub * VS < last && L::CK + (sub + 1) * VS > first) {
+                        const Rsrc r = rows16(vb + page * a.c.v_page + row * a.c.v_row, rows * a.c.v_row);
+                        each_of<0, VS>([&](auto piece) {
+                            const int i = L::CK + sub * VS + piece.value;
+                            if (i >= first && i < last) to_lds<ONCE>(r, voff[piece.value], at + i * 1024);
+                        });
+                    }
+                }
+                return;
+            }
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -640,7 +684,7 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
             if (found) odd[wave] = 1;
         };
         // A tile at LDS address `at`.
-        const auto step = [&](uint32_t at, bool whole) {
+        const auto tile = [&](uint32_t at, bool whole) {
             f32x4 sc[MT][2 * NS];
             scores(at, sc);
             if constexpr (NB == 1) {  // one tile: its keys make room for the next ones, then its values
@@ -735,11 +779,11 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
                     clean(at);            // each wave a share of its tiles, before any of them is read
                     wait_and_meet();
                 }
-                if (t0 < t_end) step(at, whole);
+                if (t0 < t_end && !idle) tile(at, whole);
                 at = next;
             } else {
                 wait_loads<(NB > 1 ? NC : NC / 2)>();  // of two tiles under way the older one (one tile: its keys)
-                step(at, whole);
+                tile(at, whole);
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 if constexpr (NB == 1) {
                     fetch(t0 + STEP, pb, at, NC / 2, NC);
@@ -805,7 +849,6 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
                 // l 2^shift < 1/2: sums stay below half of the largest value
                 shift = (float)(-1 - __builtin_amdgcn_readfirstlane(e));
                 again = true;
-                it -= (int)gridDim.x;
                 continue;
             }
             again = false;
@@ -849,7 +892,7 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
             for (int m = 0; m < MT; ++m) {
                 int rl = (rw * MT + m) * 16 + c;
                 asm volatile("" : "+v"(rl));  // addresses from it are not kept through the loops (two instances would spill)
-                const int r = p.blk * RB + rl;
+                const int r = p.r0 + rl;
                 if (r >= rows) continue;
 #pragma unroll
                 for (int w = 0; w < T - 1; ++w)
@@ -876,12 +919,19 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
                     }
                 }
                 if (!p.last) {
-                    float* to = piece_rows(ws, item, RB, D);
+                    float *to, *sums;
+                    if constexpr (MODE == kParts) {
+                        to = row_of(p, rl, p.q0 + t, hq);
+                        sums = to + D;
+                    } else {
+                        to = piece_rows(ws, p.slot, RB, D) + rl * D;
+                        sums = piece_rows(ws, p.slot, RB, D) + RB * D + 2 * rl;
+                    }
 #pragma unroll
-                    for (int e = 0; e < NE; ++e) *reinterpret_cast<f32x4*>(to + rl * D + 16 * e + 4 * j) = o[m][e] * fold[m];
+                    for (int e = 0; e < NE; ++e) *reinterpret_cast<f32x4*>(to + 16 * e + 4 * j) = o[m][e] * fold[m];
                     if (j == 0) {
-                        to[RB * D + 2 * rl] = mx[m];
-                        to[RB * D + 2 * rl + 1] = l[m];
+                        sums[0] = mx[m];
+                        sums[1] = l[m];
                     }
                     continue;
                 }
@@ -898,6 +948,7 @@ __device__ __forceinline__ void attn_pieces(const Args& a, Shared<Cfg<FP8, D, MT
         }
         __syncthreads();  // the tiles, ml, odd and o_lds are written again by the next piece
     }
+    return it;
 }
 
 // One row's sums from several pieces: lane s of a wave takes the maximum and sum of piece s, so that all pieces'
@@ -907,9 +958,9 @@ struct RowSums {
     static constexpr int N = D / 64;
     float m = -INFINITY, l = 0.f, o[N] = {};
 };
-// Adds the pieces s0, s0 + WAVES, ... of `pieces` whose blocks of rb rows begin `apart` floats from one another.
-template <int D, int WAVES>
-__device__ __forceinline__ void join_row(RowSums<D>& x, const float* rows, uint32_t apart, int pieces, int s0, int rb, int rl, float cc) {
+// Adds the pieces s0, s0 + WAVES, ... of `pieces`; row_at(i) is piece i's row, sums_at(i) its maximum and sum.
+template <int D, int WAVES, typename RowAt, typename SumsAt>
+__device__ __forceinline__ void join_row(RowSums<D>& x, int pieces, int s0, float cc, const RowAt& row_at, const SumsAt& sums_at) {
     constexpr int N = D / 64;
     const int lane = threadIdx.x & 63;
     float &m = x.m, &l = x.l;
@@ -920,7 +971,7 @@ __device__ __forceinline__ void join_row(RowSums<D>& x, const float* rows, uint3
         const auto request = [&](int k) {  // eight rows
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float* from = rows + (uint64_t)(uint32_t)(k0 + min(k + i, count - 1) * WAVES) * apart + rl * D + lane * N;
+                const float* from = row_at(k0 + min(k + i, count - 1) * WAVES) + lane * N;
 #pragma unroll
                 for (int e = 0; e < N; ++e) y[i][e] = from[e];
             }
@@ -930,7 +981,7 @@ __device__ __forceinline__ void join_row(RowSums<D>& x, const float* rows, uint3
         request(0);
         float mk = -INFINITY, lk = 0.f;
         if (lane < count) {
-            const float2 y2 = *reinterpret_cast<const float2*>(rows + (uint64_t)(uint32_t)mine * apart + rb * D + 2 * rl);
+            const float2 y2 = *reinterpret_cast<const float2*>(sums_at(mine));
             mk = y2.x;
             lk = y2.y;
         }
@@ -959,6 +1010,12 @@ __device__ __forceinline__ void join_row(RowSums<D>& x, const float* rows, uint3
             }
         }
     }
+}
+// Pieces whose blocks of rb rows (D means each, then the rows' maxima and sums) begin `apart` floats from one another.
+template <int D, int WAVES>
+__device__ __forceinline__ void join_row(RowSums<D>& x, const float* rows, uint32_t apart, int pieces, int s0, int rb, int rl, float cc) {
+    join_row<D, WAVES>(x, pieces, s0, cc, [&](int i) { return rows + (uint64_t)(uint32_t)i * apart + rl * D; },
+                       [&](int i) { return rows + (uint64_t)(uint32_t)i * apart + rb * D + 2 * rl; });
 }
 // With four waves to a row: their sums, in the first one; false in the others.
 template <int D, int WAVES>

@@ -19,12 +19,15 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
     constexpr int RB = C::RB;
     __shared__ __align__(1024) Shared<C> sh;
     const int blocks = (a.group + RB - 1) / RB, lane = threadIdx.x & 63;
-    attn_pieces<kBlocks, TQ, FP8, D, MT, R, T, NS, NB, ONCE>(a, sh, a.tokens * a.splits * blocks * a.c.heads, a.ws, [&](int item, Piece& p) {
+    const int items = a.tokens * a.splits * blocks * a.c.heads;
+    attn_pieces<kBlocks, TQ, FP8, D, MT, R, T, NS, NB, ONCE>(a, sh, blockIdx.x, a.ws, [&](int it) { return it < 8 * xcd_share(items); }, [&](int it) { return it + (int)gridDim.x; }, [&](int it, Piece& p) {
+        const int item = xcd_item(it, items);
+        if (item >= items) return false;
         int r = item / a.tokens;
         const int token = item - r * a.tokens;
         const int split = r % a.splits;
         r /= a.splits;
-        p.blk = r % blocks;
+        p.r0 = r % blocks * RB;
         p.h = r / blocks;
         const int b = find_last(a.q_start, a.batch, token);
         const Seq s = seq_at(a, b);
@@ -51,11 +54,12 @@ __global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8
         p.ctx = (p.chosen << a.c.lps) + (s.ctx & ((1 << a.c.lps) - 1));
         p.len = p.ctx + s.n;
         const int units = units_of(p.len);
-        p.splits = min(units, a.splits);
-        if (a.splits > 1 && split == 0 && p.blk == 0 && threadIdx.x == 0) a.cut[p.h * a.tokens + token] = p.splits;
-        if (split >= p.splits) return false;
-        attn_range(units, p.splits, split, &p.u0, &p.u1);
-        p.last = p.splits <= 1;
+        const int splits = min(units, a.splits);
+        if (a.splits > 1 && split == 0 && p.r0 == 0 && threadIdx.x == 0) a.cut[p.h * a.tokens + token] = splits;
+        if (split >= splits) return false;
+        attn_range(units, splits, split, &p.u0, &p.u1);
+        p.slot = item;
+        p.last = splits <= 1;
         return true;
     });
 }

@@ -195,14 +195,14 @@ int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64
     if ((st = ubw_prefix_attn_workspace_bytes(batch, groups, tokens, max_tree, heads, a.c.heads, d, &need)) != UBW_OK ||
         (st = check_workspace(workspace, ws_bytes, need, false)) != UBW_OK)
         return st;
-    a.z = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * a.group, a.group, a.c.heads, d);
-    if (a.z.cap_shared > kMaxGrid || a.z.cap_own > kMaxGrid) return UBW_ERANGE;
+    const PrefixSizes z = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * a.group, a.group, a.c.heads, d);
+    if (z.lists > kMaxGrid) return UBW_ERANGE;
     a.group_start = group_start;
     a.prefix_len = prefix_len;
     a.groups = groups;
     a.ws = static_cast<float*>(workspace);
-    a.own_at = a.z.cap_shared * a.z.rb_shared * (d + 2);
-    a.plan = reinterpret_cast<int*>(a.ws + prefix_floats(a.z, d));
+    a.plan = reinterpret_cast<int*>(a.ws + z.rows * prefix_row_floats(d));
+    a.most_lists = z.lists;
     return hip_status(launch_prefix_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
 }
 

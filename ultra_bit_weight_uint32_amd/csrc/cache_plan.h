@@ -171,48 +171,65 @@ inline int64_t attn_workspace_floats(int batch, int max_tree, int group, int kv_
 }
 
 // ---- attention over shared prefixes ---------------------------------------------------------
-// Two lists of pieces: of each group's prefix, with blocks of its tokens' rows, and of what each sequence has
-// behind it. Blocks of 128 rows (64 of 256 dims) for prefixes; for the rest 16 where a sequence has no more.
-inline AttnTile prefix_tile(int head_dim) { return AttnTile{head_dim == 256 ? 1 : 2, 4}; }
-inline AttnTile own_tile(int64_t max_rows, int head_dim) { return max_rows <= 16 ? AttnTile{1, 1} : prefix_tile(head_dim); }
+// An owner is a group, with its tokens' rows over its prefix, or a sequence, with its rows over what is behind it. Its
+// rows lie in blocks of 128 (64 of 256 dims), the last up to 32 in a block of a smaller tile; a list is a block of a
+// key/value head with the owner's positions, in units of 128. What lists cost is known well enough to deal them out
+// beforehand (trees of 1 to 16 tokens behind five prefixes of 3K to 40K positions in 8 bits: 4.0 us a unit at any
+// number of rows, with the small tile 1.5; single tokens behind one of 16K in 16 bits: 4.5 and 2.6; 8 to 10 us to begin
+// and end a piece): every one of 512 workgroups is to have the same. So lists are cut into full pieces, one to a
+// workgroup, as long as that allows, and a rest; the workgroups without a full piece share out the rests, the longest
+// first, in runs of the same cost.
+constexpr int kPrefixWgs = 512;  // two on every CU
+constexpr int kUnitCost = 7, kSmallUnitCost = 4, kSmallUnitCost8 = 3, kPieceCost = 16;  // in 0.64 us; 8: 8-bit caches
+constexpr int kSmallRows = 32;
+UBW_HD inline int prefix_rows(int head_dim) { return head_dim == 256 ? 64 : 128; }
+// What a workgroup is to have, for lists of this cost in all.
+UBW_HD inline int64_t prefix_goal(int64_t cost) { return (cost + kPrefixWgs - 1) / kPrefixWgs + kPieceCost; }
+UBW_HD inline int prefix_full(int64_t goal, int unit_cost) {  // units of a full piece
+    const int64_t n = (goal - kPieceCost) / unit_cost;
+    return (int)(n < 1 ? 1 : n < kAttnMostChunk ? n : kAttnMostChunk);
+}
+// How a list of `units` is cut: full pieces, and what is behind them (an eighth of one or less is spread over them).
+struct PrefixCut {
+    int full, rest;
+};
+UBW_HD inline PrefixCut prefix_cut(int units, int length) {
+    PrefixCut c{units / length, units % length};
+    if (c.full > 0 && c.rest <= length / 8) c.rest = 0;
+    return c;
+}
+// Full pieces: a list of u units has at most u / length of them, and length >= (goal - kPieceCost) / (2 unit_cost), so
+// that they are at most 2 cost / (cost / 512).
+constexpr int kPrefixFull = 2 * kPrefixWgs;
+// The workspace: sums of the full pieces (head_dim means, maximum, sum, two unused words a row), of the rests of each
+// (token, head) over the own positions and over the prefix; the plan: a head, sixteen words an owner, two words a piece.
+constexpr int kPlanHead = 16 + kPrefixWgs, kPlanOwner = 16;
 struct PrefixSizes {
-    int rb_shared, rb_own;          // rows of a block
-    int target_shared, target_own;  // pieces aimed at
-    int64_t blocks_shared;          // most blocks of rows of all groups and heads
-    int64_t cap_shared, cap_own;    // most pieces
+    int64_t lists;  // most lists
+    int64_t rows;   // rows of sums
+    int64_t words;  // of the plan
 };
 inline PrefixSizes prefix_sizes(int batch, int groups, int64_t tokens, int64_t max_rows, int group, int kv_heads, int head_dim) {
-    const AttnTile own = own_tile(max_rows, head_dim);
+    const int rb = prefix_rows(head_dim);
     PrefixSizes p{};
-    p.rb_shared = attn_rows(prefix_tile(head_dim));
-    p.rb_own = attn_rows(own);
-    p.target_shared = attn_target(prefix_tile(head_dim), head_dim);
-    p.target_own = attn_target(own, head_dim);
-    p.blocks_shared = groups > 0 ? (tokens * group / p.rb_shared + groups) * kv_heads : 0;
-    p.cap_shared = groups > 0 ? p.target_shared + p.blocks_shared : 0;
-    p.cap_own = attn_max_items(batch, max_rows, kv_heads, head_dim, own);
+    p.lists = ((groups > 0 ? tokens * group / rb + groups : 0) + batch * cdiv(max_rows, rb)) * kv_heads;
+    p.rows = (int64_t)kPrefixFull * rb + 2 * tokens * group * kv_heads;
+    p.words = kPlanHead + kPlanOwner * ((int64_t)groups + batch) + 2 * (kPrefixFull + p.lists);
     return p;
 }
-// The plan, in 32-bit words: the lists' sizes, five words a group and four a sequence, and the ends of both lists.
-constexpr int kPlanHead = 8;
-inline int64_t prefix_plan_words(int batch, int groups) { return kPlanHead + 6 * ((int64_t)groups + 1) + 4 * ((int64_t)batch + 1); }
-inline int64_t prefix_floats(const PrefixSizes& p, int head_dim) {
-    return (p.cap_shared * p.rb_shared + p.cap_own * p.rb_own) * (head_dim + 2);
-}
+inline int64_t prefix_row_floats(int head_dim) { return head_dim + 4; }
 inline int64_t prefix_workspace_floats(int batch, int groups, int64_t tokens, int max_tree, int group, int kv_heads, int head_dim) {
-    int64_t most = 0;
-    for (int n = 1; n <= max_tree; ++n) {
-        const int64_t x = prefix_floats(prefix_sizes(batch, groups, tokens, (int64_t)n * group, group, kv_heads, head_dim), head_dim);
-        most = x > most ? x : most;
-    }
-    return most + prefix_plan_words(batch, groups);
+    const PrefixSizes p = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * group, group, kv_heads, head_dim);
+    return p.rows * prefix_row_floats(head_dim) + p.words;
 }
 
 // ---- selected blocks ------------------------------------------------------------------------
 // Attention over them: a token and key/value head have their rows (the head's queries) and positions to
 // themselves. Their number is bounded by the list's length, which the host knows, and so is the cut.
 inline int64_t block_positions(int count, int page_size, int max_tree) { return (int64_t)count * page_size + page_size - 1 + max_tree; }
-inline AttnTile block_tile(int group, int head_dim) { return own_tile(group, head_dim); }
+inline AttnTile block_tile(int group, int head_dim) {
+    return group <= 16 ? AttnTile{1, 1} : AttnTile{head_dim == 256 ? 1 : 2, 4};
+}
 inline int64_t block_pairs(int64_t tokens, int group, int kv_heads, AttnTile t) { return tokens * kv_heads * cdiv(group, attn_rows(t)); }
 constexpr int kBlockTarget = 512;  // pieces aimed at
 inline int block_splits(int64_t pairs, int64_t positions) {

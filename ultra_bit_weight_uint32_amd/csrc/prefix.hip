@@ -4,118 +4,141 @@
 // 2^((s - m) log2 e) over a part's positions, o their weighted mean,
 //     out = sum_parts l_i 2^((m_i - m) log2 e) o_i / sum_parts l_i 2^((m_i - m) log2 e),  m = max m_i.
 //
-// Three launches: k_plan (one workgroup) measures the groups, cuts both lists into pieces (attn_pieces.h) and
-// leaves the plan in the workspace; k_prefix goes through them; k_join_parts joins each row's.
+// Three launches: k_plan (one workgroup) measures the groups, cuts the lists of rows and positions into pieces and
+// deals them out (cache_plan.h); k_prefix goes through them (attn_pieces.h); k_join_parts joins each row's.
 //   * A prefix ends at a multiple of 16 positions, so that no tile has positions of both parts; the few behind
 //     it are each sequence's own (its own row of the table has them too).
 //   * A prefix passes the shortest context of its group nowhere, so that a sequence never sees what is not its own.
+//   * Prefixes of many rows keep the vector unit and the matrix cores busy, single rows the memory: each XCD has an
+//     eighth of the full pieces, in order (row blocks over the same keys and values meet in its L2), and of the rests.
+//     Which workgroup has a piece decides nothing but the time.
 #include "attn_pieces.h"
 
 namespace ubw {
 namespace cache {
 namespace {
 
-constexpr int kPlanThreads = 1024;
-constexpr int kMost = UBW_MAX_SEQS, kEach = kMost / kPlanThreads;
+constexpr int kPlanThreads = 512;
+static_assert(kPlanThreads >= kPrefixWgs, "a thread for every workgroup of rests");
+constexpr int kBuckets = 64;  // rests are sorted by their length in 64ths of a full piece
 
-// The plan's arrays. Groups: first piece (and the end of the list), positions, table row, first token, rows, pieces a
-// row's positions are cut into. Sequences: first piece (and the end), base, group, pieces.
-struct PlanAt {
-    int *head, *g_first, *g_len, *g_row, *g_q0, *g_rows, *g_splits, *s_first, *s_base, *s_group, *s_splits;
+// An owner in the plan. Class 0: whole blocks of rows, class 1: the small one.
+struct Owner {
+    int row, q0, rows, base;  // row of the table, first token, rows, position where its units begin
+    int ctx, len, tree, big;  // ends of the context and of the positions; 0, or -1: no tree; whole blocks
+    int full0[2], full[2];    // first full piece, full pieces of a list
+    int rest[2];              // units of the rest
+    int units, group;         // of a list; a sequence's group, -1: none
 };
-__device__ __host__ inline PlanAt plan_at(int* p, int groups, int batch) {
+static_assert(sizeof(Owner) == 4 * kPlanOwner, "owners lie in the plan");
+struct Work {
+    int owner, index;  // index: class, then (part, head, block) of it; part: the full piece, or behind them the rest
+};
+struct PlanAt {
+    int* head;  // full pieces, long rests
+    int* run;   // where each workgroup's run of the other rests begins, and the end
+    Owner* owner;
+    Work* full;
+    Work* rest;
+};
+__device__ inline PlanAt plan_at(int* p, int owners) {
     PlanAt x;
     x.head = p;
-    x.g_first = p + kPlanHead;
-    x.g_len = x.g_first + groups + 1;
-    x.g_row = x.g_len + groups + 1;
-    x.g_q0 = x.g_row + groups + 1;
-    x.g_rows = x.g_q0 + groups + 1;
-    x.g_splits = x.g_rows + groups + 1;
-    x.s_first = x.g_splits + groups + 1;
-    x.s_base = x.s_first + batch + 1;
-    x.s_group = x.s_base + batch + 1;
-    x.s_splits = x.s_group + batch + 1;
+    x.run = p + 8;
+    x.owner = reinterpret_cast<Owner*>(p + kPlanHead);
+    x.full = reinterpret_cast<Work*>(x.owner + owners);
+    x.rest = x.full + kPrefixFull;
     return x;
 }
 
-// Sums of two numbers over the workgroup, for every thread.
+// Two numbers of the threads before this one, added up.
 struct Two {
-    int64_t a, b;
+    int a, b;
 };
-__device__ inline Two plan_sum(Two x, int64_t (&lds)[2][kPlanThreads / 64]) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        x.a += __shfl_xor((long long)x.a, d);
-        x.b += __shfl_xor((long long)x.b, d);
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-        lds[0][threadIdx.x >> 6] = x.a;
-        lds[1][threadIdx.x >> 6] = x.b;
-    }
-    __syncthreads();
-    Two s{0, 0};
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / 64; ++w) {
-        s.a += lds[0][w];
-        s.b += lds[1][w];
-    }
-    return s;
-}
-// Sums of the threads before this one.
-__device__ inline Two plan_before(Two mine, int64_t (&lds)[2][kPlanThreads / 64]) {
+__device__ inline Two plan_before(Two mine, Two (&lds)[kPlanThreads / 64], Two* all) {
     Two y = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up((long long)y.a, d), v = __shfl_up((long long)y.b, d);
+        const int u = __shfl_up(y.a, d), v = __shfl_up(y.b, d);
         if ((int)(threadIdx.x & 63) >= d) {
             y.a += u;
             y.b += v;
         }
     }
+    Two x{y.a - mine.a, y.b - mine.b}, t{0, 0};
+    if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = y;
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) {
-        lds[0][threadIdx.x >> 6] = y.a;
-        lds[1][threadIdx.x >> 6] = y.b;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+        const Two z = lds[w];
+        if (w < (int)(threadIdx.x >> 6)) {
+            x.a += z.a;
+            x.b += z.b;
+        }
+        t.a += z.a;
+        t.b += z.b;
     }
-    __syncthreads();
-    Two s{y.a - mine.a, y.b - mine.b};
-    for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) {
-        s.a += lds[0][w];
-        s.b += lds[1][w];
-    }
-    return s;
+    *all = t;
+    return x;
 }
-// A thread has the groups and the sequences kEach t .. kEach t + kEach - 1.
-__global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, bool one_row_wave) {
+
+// Workgroups for the rests: each XCD's that have no full piece (all, if it has as many full pieces as workgroups).
+__device__ inline int rest_bins(int full) {
+    const int per = (full + 7) >> 3;
+    return per < kPrefixWgs / 8 ? kPrefixWgs - 8 * per : kPrefixWgs;
+}
+// The n-th of the long rests that the w-th of these has: there and back.
+__device__ inline int rest_at(int n, int w, int bins) { return n * bins + (n & 1 ? bins - 1 - w : w); }
+// Blocks of `rows` rows: whole ones, and a small one. (The tile of 256 dims has no small one.)
+struct RowBlocks {
+    int big, small;
+};
+__device__ inline RowBlocks blocks_of(int rows, int lrb) {
+    const int whole = rows >> lrb, rest = rows - (whole << lrb);
+    return rest == 0 ? RowBlocks{whole, 0} : rest <= kSmallRows && lrb == 7 ? RowBlocks{whole, 1} : RowBlocks{whole + 1, 0};
+}
+
+// A thread has the groups and the sequences EACH t .. EACH t + EACH - 1.
+template <int EACH>
+__global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, int small_cost) {
+    constexpr int kMost = EACH * kPlanThreads;
     __shared__ int start[kMost + 1], len[kMost], lead[kMost], last[kMost];
-    __shared__ int64_t lds[2][kPlanThreads / 64];
+    __shared__ int bucket[kBuckets], bucket0[kBuckets + 1];     // rests, and those before
+    __shared__ float cost0[kBuckets + 1];                       // what those before cost
+    __shared__ unsigned long long cost[2];                      // of the groups' lists, of all others
+    __shared__ int lists;                                       // of the groups
+    __shared__ int full0[4 * kMost];  // first full piece of each owner's classes
+    __shared__ Two lds[kPlanThreads / 64];
+    __shared__ float rooms[kPlanThreads / 64];
     const int tid = threadIdx.x, kv = a.c.heads;
-    const PlanAt at = plan_at(a.plan, a.groups, a.batch);
-    const int per_g = (a.groups + kPlanThreads - 1) / kPlanThreads, per_s = (a.batch + kPlanThreads - 1) / kPlanThreads;
+    const PlanAt at = plan_at(a.plan, a.groups + a.batch);
     const int most = (int)min((int64_t)a.table_cols << a.c.lps, (int64_t)1 << 30);
     for (int g = tid; a.groups > 0 && g <= a.groups; g += kPlanThreads) {
         start[g] = min(max(a.group_start[g], 0), a.batch);
         if (g < a.groups) {
             len[g] = min(max(a.prefix_len[g], 0), most);
-            lead[g] = kMost;
+            lead[g] = a.batch;
             last[g] = -1;
         }
     }
-    Seq s[kEach];
-    int of[kEach];
+    if (tid < kBuckets) bucket[tid] = 0;
+    if (tid < 2) cost[tid] = 0;
+    if (tid == 2) lists = 0;
+    Seq s[EACH];
+    int of[EACH];
+    bool falls = false;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int b = tid * per_s + i;
-        s[i] = i < per_s && b < a.batch ? seq_of(a, b) : Seq{0, 0, 0};
+    for (int i = 0; i < EACH; ++i) {
+        const int b = tid * EACH + i;
+        s[i] = b < a.batch ? seq_of(a, b) : Seq{0, 0, 0};
+        falls |= b < a.batch && a.q_start[b + 1] < a.q_start[b];
     }
-    __syncthreads();
+    const bool none = __syncthreads_or(falls);  // q_start does not ascend: nothing is shared
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int b = tid * per_s + i;
+    for (int i = 0; i < EACH; ++i) {
+        const int b = tid * EACH + i;
         of[i] = -1;
-        if (s[i].n <= 0 || a.groups == 0) continue;
+        if (s[i].n <= 0 || a.groups == 0 || none) continue;
         int lo = 0, hi = a.groups;  // the last group that begins at b or before
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -129,186 +152,336 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, bool one_ro
     }
     __syncthreads();
 
-    int g_units[kEach], g_blocks[kEach];
-    Two sum{0, 0};  // units, blocks of the groups
+    // Owners 0, 2, ..: this thread's groups, 1, 3, ..: its sequences.
+    Owner x[2 * EACH];
+    RowBlocks rows[2 * EACH];
+    const auto cost_of = [&](const Owner& o, const RowBlocks& r) {
+        return (int64_t)kv * (r.big * ((int64_t)o.units * kUnitCost + kPieceCost) + r.small * ((int64_t)o.units * small_cost + kPieceCost));
+    };
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int g = tid * per_g + i;
-        g_units[i] = g_blocks[i] = 0;
-        if (i >= per_g || g >= a.groups) continue;
-        const int q0 = min(max(a.q_start[start[g]], 0), a.tokens);
-        const int q1 = min(max(a.q_start[max(start[g + 1], start[g])], q0), a.tokens);
-        const int rows = (q1 - q0) * a.group;
-        const int n = last[g] > lead[g] && rows > 0 ? len[g] & ~15 : 0;  // one sequence alone shares nothing
-        g_units[i] = units_of(n);
-        g_blocks[i] = n > 0 ? (rows + a.z.rb_shared - 1) / a.z.rb_shared : 0;
-        len[g] = n;
-        at.g_len[g] = n;
-        at.g_row[g] = min(lead[g], a.batch - 1);
-        at.g_q0[g] = q0;
-        at.g_rows[g] = rows;
-        sum.a += (int64_t)g_units[i] * g_blocks[i] * kv;
-        sum.b += (int64_t)g_blocks[i] * kv;
-    }
-    sum = plan_sum(sum, lds);  // (its barriers stand before the others read len)
-    // q_start does not ascend: the groups would have more rows than there are, nothing is shared
-    const bool none = sum.b > a.z.blocks_shared;
-    int s_units[kEach], s_blocks[kEach], base[kEach];
-    Two units{none ? 0 : sum.a, 0};
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        if (none) g_units[i] = g_blocks[i] = 0;
-        base[i] = of[i] >= 0 && !none ? len[of[i]] : 0;
-        s_blocks[i] = s[i].n > 0 ? (s[i].n * a.group + a.z.rb_own - 1) / a.z.rb_own : 0;
-        s_units[i] = s[i].n > 0 ? max(1, units_of(positions(a, s[i]) - base[i])) : 0;
-        units.b += (int64_t)s_units[i] * s_blocks[i] * kv;
-    }
-    units.b = plan_sum(Two{0, units.b}, lds).b;
-    const int goal_s = a.z.target_shared, goal_o = attn_aim(units.b, a.z.target_own, one_row_wave);
-    int chunk_s = attn_chunk(units.a, goal_s), chunk_o = attn_chunk(units.b, goal_o);
-    Two mine;
-    for (int step = 0;; ++step) {
-        mine = Two{0, 0};
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            mine.a += (int64_t)attn_splits(g_units[i], chunk_s) * g_blocks[i] * kv;
-            mine.b += (int64_t)attn_splits(s_units[i], chunk_o) * s_blocks[i] * kv;
+    for (int i = 0; i < EACH; ++i) {
+        const int g = tid * EACH + i;
+        Owner& o = x[2 * i];
+        o = Owner{};
+        rows[2 * i] = RowBlocks{0, 0};
+        if (g >= a.groups) continue;
+        o.q0 = min(max(a.q_start[start[g]], 0), a.tokens);
+        o.rows = (min(max(a.q_start[max(start[g + 1], start[g])], o.q0), a.tokens) - o.q0) * a.group;
+        const int n = last[g] > lead[g] && o.rows > 0 ? len[g] & ~15 : 0;  // one sequence alone shares nothing
+        o.row = min(lead[g], a.batch - 1);
+        o.ctx = o.len = n;
+        o.tree = o.group = -1;
+        o.units = units_of(n);
+        if (n > 0) rows[2 * i] = blocks_of(o.rows, lrb);
+        o.big = rows[2 * i].big;
+        if (n > 0) {
+            atomicAdd(&cost[0], (unsigned long long)cost_of(o, rows[2 * i]));
+            atomicAdd(&lists, (rows[2 * i].big + rows[2 * i].small) * kv);
         }
-        const Two all = plan_sum(mine, lds);
-        const bool fits_s = all.a <= goal_s, fits_o = all.b <= goal_o;
-        if (step == 4 || (fits_s && fits_o)) break;
-        if (!fits_s) chunk_s = attn_larger_chunk(chunk_s, all.a, goal_s);
-        if (!fits_o) chunk_o = attn_larger_chunk(chunk_o, all.b, goal_o);
+        len[g] = n;
     }
-    const Two before = plan_before(mine, lds);
-    int first = (int)before.a;
+    __syncthreads();
+    // groups that overlap: more lists than the workspace has room for, nothing is shared
+    const bool over = lists > a.most_lists - (int64_t)a.batch * ((a.max_tree * a.group + (1 << lrb) - 1) >> lrb) * kv;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int g = tid * per_g + i;
-        if (i >= per_g || g >= a.groups) continue;
-        const int splits = attn_splits(g_units[i], chunk_s);
-        at.g_first[g] = first;
-        at.g_splits[g] = splits;
-        first += splits * g_blocks[i] * kv;
+    for (int i = 0; i < EACH; ++i) {
+        const int b = tid * EACH + i;
+        if (over) rows[2 * i] = RowBlocks{0, 0};
+        Owner& o = x[2 * i + 1];
+        o = Owner{};
+        rows[2 * i + 1] = RowBlocks{0, 0};
+        if (b >= a.batch) continue;
+        o.row = b;
+        o.q0 = s[i].q0;
+        o.rows = s[i].n * a.group;
+        o.base = of[i] >= 0 && !over ? len[of[i]] : 0;
+        o.group = o.base > 0 ? of[i] : -1;
+        o.ctx = s[i].ctx;
+        o.len = positions(a, s[i]);
+        if (s[i].n <= 0) continue;
+        o.units = max(1, units_of(o.len - o.base));
+        rows[2 * i + 1] = blocks_of(o.rows, lrb);
+        o.big = rows[2 * i + 1].big;
+        atomicAdd(&cost[1], (unsigned long long)cost_of(o, rows[2 * i + 1]));
     }
-    int own = (int)before.b;
+    __syncthreads();
+    const int64_t goal = prefix_goal((int64_t)((over ? 0 : cost[0]) + cost[1]));
+    const int length[2] = {prefix_full(goal, kUnitCost), prefix_full(goal, small_cost)};
+    const float scale = (float)kBuckets / (float)goal;
+    Two count{0, 0}, first, all;  // full pieces of the groups, of the sequences
+    int in[2 * EACH][2];     // places in the rests' buckets
+    const auto bucket_of = [&](int rest, int c) {  // the longest first
+        return kBuckets - 1 - min((int)((float)rest * (float)(c ? small_cost : kUnitCost) * scale), kBuckets - 1);
+    };
+    // What a rest of bucket b costs.
+    const auto each_of = [&](int b) { return ((float)(kBuckets - b) - 0.5f) / scale + (float)kPieceCost; };
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int b = tid * per_s + i;
-        if (i >= per_s || b >= a.batch) continue;
-        const int splits = attn_splits(s_units[i], chunk_o);
-        at.s_first[b] = own;
-        at.s_splits[b] = splits;
-        at.s_base[b] = base[i];
-        at.s_group[b] = base[i] > 0 ? of[i] : -1;
-        own += splits * s_blocks[i] * kv;
+    for (int i = 0; i < 2 * EACH; ++i) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int lists = (c ? rows[i].small : rows[i].big) * kv;
+            const PrefixCut cut = prefix_cut(x[i].units, length[c]);
+            x[i].full[c] = lists > 0 ? cut.full : 0;
+            x[i].rest[c] = lists > 0 ? cut.rest : 0;
+            (i & 1 ? count.b : count.a) += x[i].full[c] * lists;
+            if (x[i].rest[c] > 0) in[i][c] = atomicAdd(&bucket[bucket_of(x[i].rest[c], c)], lists);
+        }
     }
-    if (tid == kPlanThreads - 1) {
-        at.head[0] = first;
-        at.head[1] = own;
+    first = plan_before(count, lds, &all);  // (the buckets are full, too)
+    if (tid < kBuckets) {
+        int y = bucket[tid];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int z = __shfl_up(y, d);
+            if (tid >= d) y += z;
+        }
+        float z = (float)bucket[tid] * each_of(tid);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const float u = __shfl_up(z, d);
+            if (tid >= d) z += u;
+        }
+        bucket0[tid + 1] = y;
+        cost0[tid + 1] = z;
+        if (tid == 0) bucket0[0] = 0, cost0[0] = 0.f;
+        if (tid == kBuckets - 1) {
+            at.head[0] = all.a + all.b;
+        }
     }
+    __syncthreads();
+    first.b += all.a;
+#pragma unroll
+    for (int i = 0; i < 2 * EACH; ++i) {
+        const int n = tid * EACH + (i >> 1), id = i & 1 ? a.groups + n : n;
+        if (n >= (i & 1 ? a.batch : a.groups)) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int lists = (c ? rows[i].small : rows[i].big) * kv;
+            int& k = i & 1 ? first.b : first.a;
+            x[i].full0[c] = k;
+            const int full = x[i].full[c] * lists;
+            full0[2 * id + c] = k;
+            k += full;
+            if (x[i].rest[c] > 0) {
+                Work* to = at.rest + bucket0[bucket_of(x[i].rest[c], c)] + in[i][c];
+                for (int j = 0; j < lists; ++j) to[j] = Work{id, c << 30 | (full + j)};
+            }
+        }
+        at.owner[id] = x[i];
+    }
+    __syncthreads();
+    for (int k = tid; k < all.a + all.b; k += kPlanThreads) {
+        int lo = 0, hi = 2 * (a.groups + a.batch);  // the last class that begins at k or before
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (full0[mid] <= k) lo = mid; else hi = mid;
+        }
+        at.full[k] = Work{lo >> 1, (lo & 1) << 30 | (k - full0[lo])};
+    }
+    // The rests for the workgroups without a full piece. Long ones, of more than a quarter of what such a workgroup is to have, go
+    // there and back over them; the others, in order, fill up what those leave free.
+    const int bins = rest_bins(all.a + all.b), rests = bucket0[kBuckets];
+    const float have = cost0[kBuckets] / (float)bins;
+    int lo = 0, hi = kBuckets;  // buckets of long ones
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (each_of(mid) > 0.25f * have) lo = mid + 1; else hi = mid;
+    }
+    const int longs = bucket0[lo], long_buckets = lo;
+    float room = 0.f;
+    if (tid < bins) {
+        room = have;
+        for (int n = 0;; ++n) {
+            const int k = rest_at(n, tid, bins);
+            if (k >= longs) break;
+            int from = 0, end = kBuckets;  // its bucket: the last that begins at k or before
+            while (end - from > 1) {
+                const int mid = (from + end) >> 1;
+                if (bucket0[mid] <= k) from = mid; else end = mid;
+            }
+            room -= each_of(from);
+        }
+        room = fmaxf(room, 0.f);
+    }
+    float y = room;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const float u = __shfl_up(y, d);
+        if ((tid & 63) >= d) y += u;
+    }
+    if ((tid & 63) == 63) rooms[tid >> 6] = y;
+    __syncthreads();
+    float before = y - room, total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+        if (w < (tid >> 6)) before += rooms[w];
+        total += rooms[w];
+    }
+    if (tid < bins) {
+        const float left = cost0[kBuckets] - cost0[long_buckets];
+        const float from = cost0[long_buckets] + (total > 0.f ? fminf(before / total, 1.f) * left : 0.f);
+        int b = long_buckets, end = kBuckets;
+        while (end - b > 1) {
+            const int mid = (b + end) >> 1;
+            if (cost0[mid] <= from) b = mid; else end = mid;
+        }
+        int k = longs;
+        if (b < kBuckets) {
+            const int n = bucket0[b + 1] - bucket0[b];
+            k = bucket0[b] + (n > 0 ? min(max((int)ceilf((from - cost0[b]) / each_of(b)), 0), n) : 0);
+        }
+        at.run[tid] = tid == 0 ? longs : max(k, longs);
+        if (tid == 0) at.run[bins] = rests;
+    }
+    if (tid == 0) at.head[1] = longs;
 }
 
-// PART: 1 the prefixes, 2 what is behind them.
-template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, int PART>
-__global__ __launch_bounds__((Cfg<FP8, D, MT, R, T, NS, NB>::kThreads), (Cfg<FP8, D, MT, R, T, NS, NB>::kSimd)) void k_prefix(PrefixArgs a) {
-    using C = Cfg<FP8, D, MT, R, T, NS, NB>;
-    constexpr int RB = C::RB;
-    __shared__ __align__(1024) Shared<C> sh;
-    const PlanAt at = plan_at(a.plan, a.groups, a.batch);
-    if constexpr (PART == 1)
-        attn_pieces<kShared, TQ, FP8, D, MT, R, T, NS, NB, false>(a, sh, scalar_words(at.head)[0], a.ws, [&](int item, Piece& p) {
-            const int g = find_last(at.g_first, a.groups, item);
-            const int rows = scalar_words(at.g_rows)[g], splits = scalar_words(at.g_splits)[g], blocks = (rows + RB - 1) / RB;
-            int r = item - scalar_words(at.g_first)[g];
-            p.blk = r % blocks;
-            r /= blocks;
-            p.h = r / splits;
-            p.row = scalar_words(at.g_row)[g];
-            p.q0 = scalar_words(at.g_q0)[g];
-            p.rows = rows;
-            p.splits = splits;
-            p.ctx = p.len = scalar_words(at.g_len)[g];
-            attn_range(units_of(p.len), splits, r % splits, &p.u0, &p.u1);
-            p.tree = p.base = 0;
-            p.last = false;
-            return true;
-        });
-    else
-        attn_pieces<kOwn, TQ, FP8, D, MT, R, T, NS, NB, (R == 1)>(a, sh, scalar_words(at.head)[1], a.ws + a.own_at, [&](int item, Piece& p) {
-            const int b = find_last(at.s_first, a.batch, item);
-            const Seq s = seq_at(a, b);
-            const int splits = scalar_words(at.s_splits)[b], blocks = (s.n * a.group + RB - 1) / RB;
-            int r = item - scalar_words(at.s_first)[b];
-            p.blk = r % blocks;
-            r /= blocks;
-            p.h = r / splits;
-            p.row = b;
-            p.q0 = s.q0;
-            p.rows = s.n * a.group;
-            p.splits = splits;
-            p.ctx = s.ctx;
-            p.len = positions(a, s);
-            p.base = scalar_words(at.s_base)[b];
-            p.tree = 0;
-            attn_range(max(1, units_of(p.len - p.base)), splits, r % splits, &p.u0, &p.u1);
-            p.last = splits <= 1 && p.base == 0;
-            return true;
-        });
+// The tile of whole blocks, and that of small ones.
+template <bool FP8, int D>
+struct Tiles {
+    static constexpr int MT = D == 256 ? 1 : 2, NS = D == 256 ? 1 : 2, NB = FP8 || D == 64 ? 2 : 1;
+    using Big = Cfg<FP8, D, MT, 4, 1, NS, 2>;
+    using Small = Cfg<FP8, D == 256 ? 64 : D, 2, 1, 4, 1, NB>;  // (256 dims: not used)
+};
+template <typename C1, typename C2>
+union SharedOf {
+    Shared<C1> big;
+    Shared<C2> small;
+};
+
+template <typename TQ, bool FP8, int D>
+__global__ __launch_bounds__(256, 2) void k_prefix(PrefixArgs a) {
+    using W = Tiles<FP8, D>;
+    constexpr int RB = W::Big::RB, ROW = D + 4;
+    static_assert(W::Big::kThreads == 256 && W::Small::kThreads == 256 && (D == 256 || W::Small::RB == kSmallRows), "tiles of one workgroup");
+    __shared__ __align__(1024) SharedOf<typename W::Big, typename W::Small> sh;
+    const PlanAt at = plan_at(a.plan, a.groups + a.batch);
+    const int full = scalar_words(at.head)[0];
+    // Workgroup (xcd, i) has the full pieces i, i + 64, .. of its XCD's eighth; those without one have the rests.
+    const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3, per = (full + 7) >> 3, wide = kPrefixWgs / 8;
+    const int mine = min(per, full - xcd * per), fulls = i < mine ? (mine - i + wide - 1) / wide : 0;
+    const int taken = per < wide ? per : 0, bin = (i - taken) * 8 + xcd;
+    const int bins = rest_bins(full), longs = scalar_words(at.head)[1];
+    int rest0 = 0, rests = 0, mine_long = 0;
+    if (i >= taken) {
+        rest0 = scalar_words(at.run)[bin];
+        rests = scalar_words(at.run)[bin + 1] - rest0;
+        while (rest_at(mine_long, bin, bins) < longs) ++mine_long;
+    }
+    // Work n of this workgroup, -1 behind the last.
+    Work work{0, 0};
+    const auto get = [&](int n) {
+        const Work* from;
+        if (n < fulls) {
+            from = at.full + xcd * per + i + n * wide;
+        } else {
+            const int k = n - fulls;
+            if (k >= mine_long + rests) return -1;
+            from = at.rest + (k < mine_long ? rest_at(k, bin, bins) : rest0 + k - mine_long);
+        }
+        const ScalarWord* w = scalar_words(reinterpret_cast<const int*>(from));
+        work = Work{w[0], w[1]};
+        return n;
+    };
+    const auto next = [&](int n) { return get(n + 1); };
+    const auto piece = [&](int, Piece& p) {
+        const ScalarWord* o = scalar_words(reinterpret_cast<const int*>(at.owner + work.owner));
+        const int c = work.index >> 30, big = o[7], blocks = c ? 1 : big, units = o[14], cut = o[10 + c], rest = o[12 + c];
+        int r = work.index & ((1 << 30) - 1);
+        const int part = r / (blocks * a.c.heads);
+        r -= part * blocks * a.c.heads;
+        p.h = r / blocks;
+        p.r0 = (c ? big : r - p.h * blocks) * RB;
+        p.row = o[0];
+        p.q0 = o[1];
+        p.rows = o[2];
+        p.base = o[3];
+        p.ctx = o[4];
+        p.len = o[5];
+        p.tree = o[6];
+        if (part < cut) attn_range(units - rest, cut, part, &p.u0, &p.u1);
+        else p.u0 = units - rest, p.u1 = units;
+        p.slot = part < cut ? o[8 + c] + (work.index & ((1 << 30) - 1)) : -1;
+        p.last = p.base == 0 && p.tree == 0 && p.u1 - p.u0 == units;
+        return true;
+    };
+    const auto row_of = [&](const Piece& p, int rl, int token, int hq) {
+        const int64_t rest = (int64_t)kPrefixFull * RB + ((p.tree < 0 ? a.tokens : 0) + (int64_t)token) * a.heads + hq;
+        return a.ws + (p.slot >= 0 ? (int64_t)p.slot * RB + rl : rest) * ROW;
+    };
+    int n = get(0);
+#pragma unroll 1
+    while (n >= 0) {
+        if (D == 256 || work.index >> 30 == 0) {
+            n = attn_pieces<kParts, TQ, FP8, D, W::MT, 4, 1, W::NS, 2, false>(
+                a, sh.big, n, a.ws, [&](int n) { return n >= 0 && (D == 256 || work.index >> 30 == 0); }, next, piece, row_of);
+        } else if constexpr (D < 256) {
+            n = attn_pieces<kParts, TQ, FP8, D, 2, 1, 4, 1, W::NB, true>(
+                a, sh.small, n, a.ws, [&](int n) { return n >= 0 && work.index >> 30 != 0; }, next, piece, row_of);
+        }
+    }
 }
 
 // Joins the pieces of the prefix and of what is behind it, WAVES waves per (token, query head), in an order that
-// does not depend on timing.
+// does not depend on timing: the prefix's full pieces and rest, the own ones.
 template <typename TQ, int D, int WAVES>
 __global__ __launch_bounds__(256) void k_join_parts(PrefixArgs a) {
+    constexpr int RB = D == 256 ? 64 : 128, ROW = D + 4;
     __shared__ float part[4][D + 2];
     const int wave = threadIdx.x >> 6;
     const int b = blockIdx.x / a.c.heads, h = blockIdx.x - b * a.c.heads;
     const int r = WAVES == 4 ? (int)blockIdx.y : (int)blockIdx.y * 4 + wave;
-    const PlanAt at = plan_at(a.plan, a.groups, a.batch);
-    const Seq s = seq_at(a, b);
-    const int own = scalar_words(at.s_splits)[b], g = scalar_words(at.s_group)[b];
-    if ((own <= 1 && g < 0) || r >= s.n * a.group) return;
-    const int s0 = WAVES == 4 ? wave : 0;
+    const PlanAt at = plan_at(a.plan, a.groups + a.batch);
+    const ScalarWord* o = scalar_words(reinterpret_cast<const int*>(at.owner + a.groups + b));
+    if (r >= (int)o[2]) return;
+    const int q0 = o[1], g = o[15], t = r / a.group, hq = h * a.group + (r - t * a.group);
+    // where the pieces of row x of an owner are
+    struct Rows {
+        const float *full, *rest;
+        uint32_t apart;
+        int n, all;
+    };
+    const auto rows_at = [&](const ScalarWord* o, int x, bool shared) {
+        const int big = o[7], blk = x / RB, c = blk >= big, blocks = c ? 1 : big, n = o[10 + c];
+        Rows y;
+        y.full = a.ws + ((int64_t)(o[8 + c] + h * blocks + (c ? 0 : blk)) * RB + (x - blk * RB)) * ROW;
+        y.rest = a.ws + ((int64_t)kPrefixFull * RB + ((shared ? a.tokens : 0) + (int64_t)(q0 + t)) * a.heads + hq) * ROW;
+        y.apart = (uint32_t)(a.c.heads * blocks * RB * ROW);
+        y.n = n;
+        y.all = n + (o[12 + c] > 0);
+        return y;
+    };
+    const Rows own = rows_at(o, r, false);
+    if (own.all <= 1 && g < 0) return;
+    Rows group{};
+    if (g >= 0) {
+        const ScalarWord* go = scalar_words(reinterpret_cast<const int*>(at.owner + g));
+        const int x = (q0 - (int)go[1]) * a.group + r;
+        if (x >= 0 && x < (int)go[2]) group = rows_at(go, x, true);
+    }
     const float scale = a.scale * (a.c.k_scale ? a.c.k_scale[h] : 1.f);
     const float unit = ldexpf(scale, -lower<TQ>(scale)), cc = unit * kLog2e;  // as in attn_pieces
+    const auto row = [&](int i) {
+        const bool mine = i >= group.all;
+        const int k = mine ? i - group.all : i, n = mine ? own.n : group.n;
+        const float* full = mine ? own.full : group.full;
+        return k < n ? full + (uint64_t)(uint32_t)k * (mine ? own.apart : group.apart) : mine ? own.rest : group.rest;
+    };
     RowSums<D> x;
-    if (g >= 0) {
-        const int rows = scalar_words(at.g_rows)[g], splits = scalar_words(at.g_splits)[g], rb = a.z.rb_shared;
-        const int rp = (s.q0 - scalar_words(at.g_q0)[g]) * a.group + r, blocks = (rows + rb - 1) / rb;
-        if (rp >= 0 && rp < rows)
-            join_row<D, WAVES>(x, piece_rows(a.ws, scalar_words(at.g_first)[g] + h * splits * blocks + rp / rb, rb, D),
-                               (uint32_t)(blocks * rb * (D + 2)), splits, s0, rb, rp % rb, cc);
-    }
-    const int rb = a.z.rb_own, blocks = (s.n * a.group + rb - 1) / rb;
-    join_row<D, WAVES>(x, piece_rows(a.ws + a.own_at, scalar_words(at.s_first)[b] + h * own * blocks + r / rb, rb, D),
-                       (uint32_t)(blocks * rb * (D + 2)), own, s0, rb, r % rb, cc);
+    join_row<D, WAVES>(x, group.all + own.all, WAVES == 4 ? wave : 0, cc, row, [&](int i) { return row(i) + D; });
     if constexpr (WAVES == 4) {
         if (!join_waves<D, WAVES>(x, part, cc)) return;
     }
-    const int t = r / a.group;
-    store_row<TQ, D>(a, x, s.q0 + t, h, r - t * a.group, unit);
+    store_row<TQ, D>(a, x, q0 + t, h, r - t * a.group, unit);
 }
 
-template <typename TQ, bool FP8, int D, int MT, int R, int T, int NS, int NB, int PART>
-void launch_part(const PrefixArgs& a, int64_t most, hipStream_t s) {
-    using C = Cfg<FP8, D, MT, R, T, NS, NB>;
-    const int64_t wgs = most < kCus * C::kPerCu ? cdiv(most, 8) * 8 : kCus * C::kPerCu;
-    k_prefix<TQ, FP8, D, MT, R, T, NS, NB, PART><<<(unsigned)wgs, C::kThreads, 0, s>>>(a);
-}
 template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const PrefixArgs& a, hipStream_t s) {
-    const bool few = a.z.rb_own == 16;
-    k_plan<<<1, kPlanThreads, 0, s>>>(a, few);
-    if constexpr (D == 256) {
-        if (a.groups > 0) launch_part<TQ, FP8, D, 1, 4, 1, 1, 2, 1>(a, a.z.cap_shared, s);
-        if (few) launch_part<TQ, FP8, D, 1, 1, 2, 1, FP8 ? 2 : 1, 2>(a, a.z.cap_own, s);
-        else launch_part<TQ, FP8, D, 1, 4, 1, 1, 2, 2>(a, a.z.cap_own, s);
-    } else {
-        if (a.groups > 0) launch_part<TQ, FP8, D, 2, 4, 1, 2, 2, 1>(a, a.z.cap_shared, s);
-        if (few) launch_part<TQ, FP8, D, 1, 1, 4, 1, FP8 || D == 64 ? 2 : 1, 2>(a, a.z.cap_own, s);
-        else launch_part<TQ, FP8, D, 2, 4, 1, 2, 2, 2>(a, a.z.cap_own, s);
-    }
+    const int most = a.batch > a.groups ? a.batch : a.groups, lrb = log2_of(prefix_rows(D)), cost = FP8 ? kSmallUnitCost8 : kSmallUnitCost;
+    if (most <= kPlanThreads) k_plan<1><<<1, kPlanThreads, 0, s>>>(a, lrb, cost);
+    else if (most <= 2 * kPlanThreads) k_plan<2><<<1, kPlanThreads, 0, s>>>(a, lrb, cost);
+    else k_plan<8><<<1, kPlanThreads, 0, s>>>(a, lrb, cost);
+    k_prefix<TQ, FP8, D><<<kPrefixWgs, 256, 0, s>>>(a);
     const int64_t rows = (int64_t)a.max_tree * a.group, pairs = (int64_t)a.batch * a.c.heads;
     if (rows * pairs <= 1024)
         k_join_parts<TQ, D, 4><<<dim3((unsigned)pairs, (unsigned)rows), 256, 0, s>>>(a);

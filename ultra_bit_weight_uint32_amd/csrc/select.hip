@@ -101,14 +101,25 @@ __global__ __launch_bounds__(256) void k_bounds(BoundsArgs a) {
         if ((uint32_t)page >= (uint32_t)a.c.pages) continue;
         const char* k = a.c.k + layer * a.c.k_layer + page * a.c.k_page + h * a.c.k_head + lane * 16;
         float lo[E::N], hi[E::N];
-        for (int r0 = 0; r0 < rows; r0 += AHEAD) {
-            u32x4 w[AHEAD];
+        u32x4 w[2 * AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) w[i] = *reinterpret_cast<const u32x4*>(k + (int64_t)(r0 + i) * a.c.k_row);
+        for (int i = 0; i < 2 * AHEAD; ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + (int64_t)i * a.c.k_row));
+        for (int r0 = 0; r0 < rows; r0 += AHEAD) {
+            u32x4 now[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                now[i] = w[i];
+                w[i] = w[AHEAD + i];
+            }
+            if (r0 + 2 * AHEAD < rows) {  // requested before these are looked at
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    w[AHEAD + i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + (int64_t)(r0 + 2 * AHEAD + i) * a.c.k_row));
+            }
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 float x[E::N];
-                E::read(w[i], x);
+                E::read(now[i], x);
 #pragma unroll
                 for (int e = 0; e < E::N; ++e) {  // (a NaN stays one)
                     lo[e] = r0 + i == 0 ? x[e] : __builtin_elementwise_minimum(lo[e], x[e]);
@@ -151,6 +162,26 @@ __device__ inline void up_down(const SelectArgs& a, int token, int h, int d, int
     }
     *up = u;
     *down = v;
+}
+// The same of eight dims, whose rows are requested together.
+template <typename TQ>
+__device__ inline void up_down8(const SelectArgs& a, int token, int h, int d, int dims, double* up, double* down) {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)token * a.ldq + (int64_t)h * a.group * dims + d;
+    for (int g0 = 0; g0 < a.group; g0 += 8) {
+        u32x4 w[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) w[g] = *reinterpret_cast<const u32x4*>(q + (int64_t)min(g0 + g, a.group - 1) * dims);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            if (g0 + g >= a.group) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double x = wide<TQ>((uint16_t)(w[g][e >> 1] >> (16 * (e & 1))));
+                up[e] += x < 0 ? 0 : x;
+                down[e] += x > 0 ? 0 : x;
+            }
+        }
+    }
 }
 // Scores as whole numbers of the same order: a NaN is the largest, both zeros are one, 0 is below all.
 __device__ inline uint64_t key_of(double x) {
@@ -236,45 +267,66 @@ __global__ __launch_bounds__(256) void k_scores_tree(SelectArgs a) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
     for (int t0 = 0; t0 < s.n; t0 += 16) {
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * D; i += 256) {
-            const int t = i / D, d = i % D, piece = d / E::N;
-            double u = 0, v = 0;
-            if (t0 + t < s.n) up_down<TQ>(a, s.q0 + t0 + t, h, d, D, &u, &v);
-            const int at = piece / 4 * E::N + d % E::N, to = piece % 4 * 16 + t;
-            q[0][at][to] = v;
-            q[1][at][to] = u;
+        for (int i = threadIdx.x; i < 2 * D; i += 256) {  // eight dims of a token
+            const int t = i / (D / 8), d = i % (D / 8) * 8, piece = d / E::N;
+            double u[8] = {}, v[8] = {};
+            if (t0 + t < s.n) up_down8<TQ>(a, s.q0 + t0 + t, h, d, D, u, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = piece / 4 * E::N + (d + e) % E::N, to = piece % 4 * 16 + t;
+                q[0][at][to] = v[e];
+                q[1][at][to] = u[e];
+            }
         }
         __syncthreads();
-        for (int i = 0; i < TILES; ++i) {
+        for (int i = 0; i < TILES; i += 2) {  // two tiles at a time share the tokens' sums
             const int first = c0 + (wave * TILES + i) * 16;
             if (first >= s.whole) break;
-            const int page = first + c < s.whole ? a.table[b * a.ld_table + first + c] : -1;
-            const bool there = (uint32_t)page < (uint32_t)a.pages;
-            const char* at = static_cast<const char*>(a.bounds) + ((int64_t)(there ? page : 0) * a.kv + h) * (2 * D * E::kSize) + j * 16;
-            f64x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            u32x4 w[2][S];
+            int page[2];
+            const char* at[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int k = 0; k < 2; ++k) {
+                const int x = first + 16 * k + c;
+                page[k] = x < s.whole ? a.table[b * a.ld_table + x] : -1;
+                if ((uint32_t)page[k] >= (uint32_t)a.pages) page[k] = -1;
+                at[k] = static_cast<const char*>(a.bounds) + ((int64_t)max(page[k], 0) * a.kv + h) * (2 * D * E::kSize) + j * 16;
+            }
+            f64x4 sum[2][2] = {};  // of each tile, lower and upper bounds
+            u32x4 w[2][2][S];
 #pragma unroll
-                for (int k = 0; k < S; ++k) w[x][k] = *reinterpret_cast<const u32x4*>(at + x * D * E::kSize + k * 64);
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < S; ++k)
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float y[E::N];
-                    E::read(w[x][k], y);
+                    for (int n = 0; n < S; ++n) w[k][x][n] = *reinterpret_cast<const u32x4*>(at[k] + x * D * E::kSize + n * 64);
 #pragma unroll
-                    for (int e = 0; e < E::N; ++e)
-                        sum[x] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)y[e], q[x][k * E::N + e][lane], sum[x], 0, 0, 0);
-                }
+            for (int n = 0; n < S; ++n) {
+                float y[2][2][E::N];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) E::read(w[k][x][n], y[k][x]);
+#pragma unroll
+                for (int e = 0; e < E::N; ++e)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const double t = q[x][n * E::N + e][lane];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            sum[k][x] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)y[k][x][e], t, sum[k][x], 0, 0, 0);
+                    }
+            }
             // lane (t, j) has the blocks j, j + 4, .. of token t
-            const uint64_t all = __ballot(there);
-            if (t0 + c < s.n) {
-                uint64_t* keys = a.keys + ((int64_t)(s.q0 + t0 + c) * a.kv + h) * a.stride + first;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int x = 4 * r + j;
-                    if (first + x < s.whole) keys[x] = (all >> x) & 1 ? key_of(sum[0][r] + sum[1][r]) : 0;
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t all = __ballot(page[k] >= 0);
+                if (t0 + c < s.n) {
+                    uint64_t* keys = a.keys + ((int64_t)(s.q0 + t0 + c) * a.kv + h) * a.stride + first + 16 * k;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int x = 4 * r + j;
+                        if (first + 16 * k + x < s.whole) keys[x] = (all >> x) & 1 ? key_of(sum[k][0][r] + sum[k][1][r]) : 0;
+                    }
                 }
             }
         }
@@ -282,7 +334,7 @@ __global__ __launch_bounds__(256) void k_scores_tree(SelectArgs a) {
 }
 
 // ---- the choice
-constexpr int kSelThreads = 512, kSelEach = 8, kSelWaves = kSelThreads / 64, kBuckets = 2048;
+constexpr int kSelThreads = 256, kSelEach = 16, kSelWaves = kSelThreads / 64, kBuckets = 2048;
 struct Chosen {
     uint64_t key;
     int at;  // the last block that is in: larger keys are, and this one up to here
