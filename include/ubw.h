@@ -580,10 +580,11 @@ int ubw_page_bounds(const ubw_kv_cache* cache, void* bounds, const int32_t* tabl
 /*
  * The choice: for each token t and key/value head h, `count` whole blocks of its sequence's context. The score of a
  * block with bounds lo, hi is
- *   sum over h's query heads g and dims d of max(q[t][g][d] lo[d], q[t][g][d] hi[d]),
- * summed in 64 bits: no sum over g of q[t][g] . k for a key k of the block is larger. The first `first` and the last
- * `last` whole blocks are always chosen, then those of the largest scores (a NaN counts as the largest; equal ones:
- * the lowest index first). Contexts of `count` whole blocks or fewer have all of them chosen.
+ *   sum over h's query heads g and dims d of max(q[t][g][d] lo[d], q[t][g][d] hi[d])
+ * (an element of q that is 0 adds nothing, whatever the bounds), summed in 64 bits: no sum over g of q[t][g] . k for a
+ * key k of the block is larger. The first `first` and the last `last` whole blocks are always chosen, then those of the
+ * largest scores (a NaN counts as the largest; equal ones: the lowest index first). Contexts of `count` whole blocks or
+ * fewer have all of them chosen.
  *   bounds   of one layer, [pages][kv_heads][2][head_dim] of type dtype, as ubw_page_bounds leaves them. (k_scale, one
  *            factor for all blocks of a head, does not change the choice.)
  *   q        q_dtype (UBW_F16 or UBW_BF16; dtype unless that is UBW_E4M3), rows as in ubw_tree_attn

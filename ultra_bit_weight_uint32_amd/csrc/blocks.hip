@@ -105,11 +105,11 @@ template <typename TQ, bool FP8, int D>
 hipError_t launch_t(const BlockArgs& a, hipStream_t s) {
     const bool few = attn_rows(block_tile(a.group, D)) == 16;
     if constexpr (D == 256) {
-        constexpr int NB = FP8 ? 2 : 1;
+        constexpr int NB = 1;
         if (few) return a.max_tree == 1 ? launch<TQ, FP8, D, 1, 1, 2, 1, NB, true>(a, s) : launch<TQ, FP8, D, 1, 1, 2, 1, NB, false>(a, s);
         return launch<TQ, FP8, D, 1, 4, 1, 1, 2, false>(a, s);
     } else {
-        constexpr int NB = FP8 || D == 64 ? 2 : 1;
+        constexpr int NB = 1;
         if (few) return a.max_tree == 1 ? launch<TQ, FP8, D, 1, 1, 4, 1, NB, true>(a, s) : launch<TQ, FP8, D, 1, 1, 4, 1, NB, false>(a, s);
         return launch<TQ, FP8, D, 2, 4, 1, 2, 2, false>(a, s);
     }

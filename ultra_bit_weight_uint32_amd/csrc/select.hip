@@ -8,7 +8,8 @@
 // which no sum over g of q_g k for a key k of the block passes. The right side costs 2 D products a block, however
 // many query heads there are. Sums are 64 bits wide: the choice then depends on the values alone, not on the order of
 // summing (in 32 bits blocks next to the border would change sides with it), and the vector unit does them at the
-// rate of 32 bits.
+// rate of 32 bits. Where lo or hi is infinite and its factor 0 the right side is no number, though the left one may be:
+// scores that are NaN are taken again without the products with 0.
 // k_select: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits.
 #include "cache_internal.h"
 
@@ -248,6 +249,16 @@ __global__ __launch_bounds__(256) void k_scores(SelectArgs a) {
 #pragma unroll
         for (int e = 0; e < E::N; ++e) sum = fma((double)y[e], u[e], fma((double)x[e], v[e], sum));
         sum = group_sum<P>(sum);
+        if (__any(sum != sum)) {
+            double again = 0;
+#pragma unroll
+            for (int e = 0; e < E::N; ++e) {
+                if (u[e] != 0) again = fma((double)y[e], u[e], again);
+                if (v[e] != 0) again = fma((double)x[e], v[e], again);
+            }
+            again = group_sum<P>(again);
+            if (sum != sum) sum = again;
+        }
         const int c = c0 + (i * 4 + wave) * B + lane / P;
         if (part == 0 && c < s.whole) keys[c] = (uint32_t)page[i] < (uint32_t)a.pages ? key_of(sum) : 0;
     }
@@ -325,7 +336,25 @@ __global__ __launch_bounds__(256) void k_scores_tree(SelectArgs a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int x = 4 * r + j;
-                        if (first + 16 * k + x < s.whole) keys[x] = (all >> x) & 1 ? key_of(sum[k][0][r] + sum[k][1][r]) : 0;
+                        if (first + 16 * k + x >= s.whole) continue;
+                        double score = sum[k][0][r] + sum[k][1][r];
+                        if (score != score && (all >> x) & 1) {
+                            const int64_t pg = a.table[b * a.ld_table + first + 16 * k + x];
+                            const char* from = static_cast<const char*>(a.bounds) + (pg * a.kv + h) * (2 * D * E::kSize);
+                            score = 0;
+#pragma unroll 1
+                            for (int i = 0; i < 2 * D / E::N; ++i) {
+                                const int half = i / (D / E::N), piece = i % (D / E::N);
+                                float y[E::N];
+                                E::read(*reinterpret_cast<const u32x4*>(from + i * 16), y);
+#pragma unroll
+                                for (int e = 0; e < E::N; ++e) {
+                                    const double t = q[half][piece / 4 * E::N + e][piece % 4 * 16 + c];
+                                    if (t != 0) score = fma((double)y[e], t, score);
+                                }
+                            }
+                        }
+                        keys[x] = (all >> x) & 1 ? key_of(score) : 0;
                     }
                 }
             }
