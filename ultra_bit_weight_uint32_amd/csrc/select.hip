@@ -146,9 +146,9 @@ __device__ inline Rows rows_of(const SelectArgs& a, int b) {
     return r;
 }
 template <typename TQ>
-__device__ inline double wide(uint16_t w) {
-    if constexpr (__is_same(TQ, _Float16)) return (double)(float)__builtin_bit_cast(_Float16, w);
-    else return (double)__builtin_bit_cast(float, (uint32_t)w << 16);
+__device__ inline float number(uint16_t w) {
+    if constexpr (__is_same(TQ, _Float16)) return (float)__builtin_bit_cast(_Float16, w);
+    else return __builtin_bit_cast(float, (uint32_t)w << 16);
 }
 // up and down of one dim of a token and key/value head
 template <typename TQ>
@@ -157,9 +157,9 @@ __device__ inline void up_down(const SelectArgs& a, int token, int h, int d, int
     double u = 0, v = 0;
 #pragma unroll 8
     for (int g = 0; g < a.group; ++g) {
-        const double x = wide<TQ>(q[(int64_t)g * dims]);
-        u += x < 0 ? 0 : x;  // (a NaN in both)
-        v += x > 0 ? 0 : x;
+        const float x = number<TQ>(q[(int64_t)g * dims]);
+        u += __builtin_elementwise_maximum(x, 0.0f);  // (a NaN in both)
+        v += __builtin_elementwise_minimum(x, 0.0f);
     }
     *up = u;
     *down = v;
@@ -177,9 +177,9 @@ __device__ inline void up_down8(const SelectArgs& a, int token, int h, int d, in
             if (g0 + g >= a.group) break;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const double x = wide<TQ>((uint16_t)(w[g][e >> 1] >> (16 * (e & 1))));
-                up[e] += x < 0 ? 0 : x;
-                down[e] += x > 0 ? 0 : x;
+                const float x = number<TQ>((uint16_t)(w[g][e >> 1] >> (16 * (e & 1))));
+                up[e] += __builtin_elementwise_maximum(x, 0.0f);  // (a NaN in both)
+                down[e] += __builtin_elementwise_minimum(x, 0.0f);
             }
         }
     }
@@ -188,6 +188,25 @@ __device__ inline void up_down8(const SelectArgs& a, int token, int h, int d, in
 __device__ inline uint64_t key_of(double x) {
     const uint64_t w = __builtin_bit_cast(uint64_t, x + 0.0);
     return x != x ? ~0ull : w >> 63 ? ~w : w | 1ull << 63;
+}
+// A block's score by one lane, without the products whose factor is 0. (Kept out of the loops, whose registers it
+// would cost.)
+template <int DT, int D, typename F>
+__device__ inline double without_zeros(const SelectArgs& a, int64_t page, int h, const F& factor) {
+    using E = Elems<DT>;
+    const char* at = static_cast<const char*>(a.bounds) + (page * a.kv + h) * (2 * D * E::kSize);
+    double sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2 * D; i += E::N) {
+        float y[E::N];
+        E::read(*reinterpret_cast<const u32x4*>(at + i * E::kSize), y);
+#pragma unroll
+        for (int e = 0; e < E::N; ++e) {
+            const double t = factor(i / D, i % D + e);
+            if (t != 0) sum = fma((double)y[e], t, sum);
+        }
+    }
+    return sum;
 }
 template <int CTRL>
 __device__ inline double moved(double x) {
@@ -239,28 +258,30 @@ __global__ __launch_bounds__(256) void k_scores(SelectArgs a) {
         u[e] = up[part * E::N + e];
         v[e] = down[part * E::N + e];
     }
-    uint64_t* keys = a.keys + ((int64_t)s.q0 * a.kv + h) * a.stride;
+    double sum[STEPS];
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         float x[E::N], y[E::N];
         E::read(lo[i], x);
         E::read(hi[i], y);
-        double sum = 0;
+        sum[i] = 0;
 #pragma unroll
-        for (int e = 0; e < E::N; ++e) sum = fma((double)y[e], u[e], fma((double)x[e], v[e], sum));
-        sum = group_sum<P>(sum);
-        if (__any(sum != sum)) {
-            double again = 0;
+        for (int e = 0; e < E::N; ++e) sum[i] = fma((double)y[e], u[e], fma((double)x[e], v[e], sum[i]));
+        sum[i] = group_sum<P>(sum[i]);
+        odd = odd || sum[i] != sum[i];
+    }
+    if (part != 0) return;
+    uint64_t* keys = a.keys + ((int64_t)s.q0 * a.kv + h) * a.stride;
 #pragma unroll
-            for (int e = 0; e < E::N; ++e) {
-                if (u[e] != 0) again = fma((double)y[e], u[e], again);
-                if (v[e] != 0) again = fma((double)x[e], v[e], again);
-            }
-            again = group_sum<P>(again);
-            if (sum != sum) sum = again;
-        }
+    for (int i = 0; i < STEPS; ++i) {
         const int c = c0 + (i * 4 + wave) * B + lane / P;
-        if (part == 0 && c < s.whole) keys[c] = (uint32_t)page[i] < (uint32_t)a.pages ? key_of(sum) : 0;
+        const bool ok = (uint32_t)page[i] < (uint32_t)a.pages;
+        if (odd && ok) {
+            const double again = without_zeros<DT, D>(a, page[i], h, [&](int half, int d) { return half ? up[d] : down[d]; });
+            if (sum[i] != sum[i]) sum[i] = again;
+        }
+        if (c < s.whole) keys[c] = ok ? key_of(sum[i]) : 0;
     }
 }
 
@@ -338,22 +359,10 @@ __global__ __launch_bounds__(256) void k_scores_tree(SelectArgs a) {
                         const int x = 4 * r + j;
                         if (first + 16 * k + x >= s.whole) continue;
                         double score = sum[k][0][r] + sum[k][1][r];
-                        if (score != score && (all >> x) & 1) {
-                            const int64_t pg = a.table[b * a.ld_table + first + 16 * k + x];
-                            const char* from = static_cast<const char*>(a.bounds) + (pg * a.kv + h) * (2 * D * E::kSize);
-                            score = 0;
-#pragma unroll 1
-                            for (int i = 0; i < 2 * D / E::N; ++i) {
-                                const int half = i / (D / E::N), piece = i % (D / E::N);
-                                float y[E::N];
-                                E::read(*reinterpret_cast<const u32x4*>(from + i * 16), y);
-#pragma unroll
-                                for (int e = 0; e < E::N; ++e) {
-                                    const double t = q[half][piece / 4 * E::N + e][piece % 4 * 16 + c];
-                                    if (t != 0) score = fma((double)y[e], t, score);
-                                }
-                            }
-                        }
+                        if (score != score && (all >> x) & 1)
+                            score = without_zeros<DT, D>(a, a.table[b * a.ld_table + first + 16 * k + x], h, [&](int half, int d) {
+                                return q[half][d / E::N / 4 * E::N + d % E::N][d / E::N % 4 * 16 + c];
+                            });
                         keys[x] = (all >> x) & 1 ? key_of(score) : 0;
                     }
                 }
