@@ -545,7 +545,8 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
  *   workspace    ubw_prefix_attn_workspace_bytes() bytes, for as many tokens as the call has or more; always
  *                needed. It needs no initialization and keeps nothing between calls; calls that may run at the
  *                same time need their own.
- *   Everything else as ubw_tree_attn. (Where q_start does not ascend nothing is shared.)
+ *   Everything else as ubw_tree_attn. (Where q_start or group_start does not ascend nothing is
+ *                shared.)
  * tokens = 0 or batch = 0 enqueues nothing.
  * Errors: as ubw_tree_attn; UBW_ERANGE (groups, tokens * heads / kv_heads above 2^30).
  */

@@ -65,6 +65,22 @@ def test_bounds(dtype, dim, page, kv, layers):
         assert torch.equal(bits(got), bits(want))
 
 
+@pytest.mark.parametrize("dtype,least", [(F16, 2.0 ** -24), (BF16, 2.0 ** -133), (E4M3, 2.0 ** -9)], ids=str)
+def test_bounds_and_choice_of_the_smallest_values(dtype, least):
+    """Multiples of the type's smallest value, which have no full mantissa."""
+    g = gen(2)
+    k = torch.randint(-7, 8, (6, 2, 16, 128), device=DEV, generator=g).double().mul(least).to(F32).to(dtype)
+    cache = ubw.KVCache(k, k)
+    got = torch.full((6, 2, 2, 128), 1.0, device=DEV).to(dtype)
+    ubw.page_bounds(cache, got, i32([[3, 0, 1, 5, 2, 4]]), i32([0]), i32([96]))
+    f = k.cpu().float()
+    assert torch.equal(got.cpu().float(), torch.stack((f.amin(2), f.amax(2)), 2)) and got.float().ne(0).any()
+    qt = F16 if dtype is E4M3 else dtype
+    for tokens in (1, 3):
+        q = torch.randint(-7, 8, (tokens, 4, 128), device=DEV, generator=g).double().mul(torch.finfo(qt).smallest_normal / 8)
+        select_and_check(q.to(F32).to(qt), got, i32([[3, 0, 1, 5, 2, 4]]), [0, tokens], [96], 3, 16, 0, 0)
+
+
 def test_bounds_of_many_pages():
     """More pages than the launch has groups of lanes, so that each takes several; far rows of a large cache."""
     g = gen(1)

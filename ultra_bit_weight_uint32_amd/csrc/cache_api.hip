@@ -202,7 +202,6 @@ int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64
     a.groups = groups;
     a.ws = static_cast<float*>(workspace);
     a.plan = reinterpret_cast<int*>(a.ws + z.rows * prefix_row_floats(d));
-    a.most_lists = z.lists;
     return hip_status(launch_prefix_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
 }
 

@@ -77,7 +77,6 @@ struct PrefixArgs : AttnArgs {
     const int32_t *group_start, *prefix_len;
     int groups;
     int* plan;  // behind the sums
-    int64_t most_lists;
 };
 hipError_t launch_prefix_attn(const PrefixArgs& a, int cache_dtype, int q_dtype, int head_dim, hipStream_t s);
 

@@ -105,15 +105,16 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
     __shared__ int start[kMost + 1], len[kMost], lead[kMost], last[kMost];
     __shared__ int bucket[kBuckets], bucket0[kBuckets + 1];     // rests, and those before
     __shared__ float cost0[kBuckets + 1];                       // what those before cost
-    __shared__ unsigned long long cost[2];                      // of the groups' lists, of all others
-    __shared__ int lists;                                       // of the groups
+    __shared__ unsigned long long cost;                         // of all lists
     __shared__ int full0[4 * kMost];  // first full piece of each owner's classes
     __shared__ Two lds[kPlanThreads / 64];
     __shared__ float rooms[kPlanThreads / 64];
     const int tid = threadIdx.x, kv = a.c.heads;
     const PlanAt at = plan_at(a.plan, a.groups + a.batch);
     const int most = (int)min((int64_t)a.table_cols << a.c.lps, (int64_t)1 << 30);
+    bool falls = false;
     for (int g = tid; a.groups > 0 && g <= a.groups; g += kPlanThreads) {
+        falls |= g > 0 && a.group_start[g] < a.group_start[g - 1];
         start[g] = min(max(a.group_start[g], 0), a.batch);
         if (g < a.groups) {
             len[g] = min(max(a.prefix_len[g], 0), most);
@@ -122,18 +123,16 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
         }
     }
     if (tid < kBuckets) bucket[tid] = 0;
-    if (tid < 2) cost[tid] = 0;
-    if (tid == 2) lists = 0;
+    if (tid == 0) cost = 0;
     Seq s[EACH];
     int of[EACH];
-    bool falls = false;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int b = tid * EACH + i;
         s[i] = b < a.batch ? seq_of(a, b) : Seq{0, 0, 0};
         falls |= b < a.batch && a.q_start[b + 1] < a.q_start[b];
     }
-    const bool none = __syncthreads_or(falls);  // q_start does not ascend: nothing is shared
+    const bool none = __syncthreads_or(falls);  // these do not ascend: nothing is shared
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int b = tid * EACH + i;
@@ -174,19 +173,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
         o.units = units_of(n);
         if (n > 0) rows[2 * i] = blocks_of(o.rows, lrb);
         o.big = rows[2 * i].big;
-        if (n > 0) {
-            atomicAdd(&cost[0], (unsigned long long)cost_of(o, rows[2 * i]));
-            atomicAdd(&lists, (rows[2 * i].big + rows[2 * i].small) * kv);
-        }
+        if (n > 0) atomicAdd(&cost, (unsigned long long)cost_of(o, rows[2 * i]));
         len[g] = n;
     }
     __syncthreads();
-    // groups that overlap: more lists than the workspace has room for, nothing is shared
-    const bool over = lists > a.most_lists - (int64_t)a.batch * ((a.max_tree * a.group + (1 << lrb) - 1) >> lrb) * kv;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int b = tid * EACH + i;
-        if (over) rows[2 * i] = RowBlocks{0, 0};
         Owner& o = x[2 * i + 1];
         o = Owner{};
         rows[2 * i + 1] = RowBlocks{0, 0};
@@ -194,7 +187,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
         o.row = b;
         o.q0 = s[i].q0;
         o.rows = s[i].n * a.group;
-        o.base = of[i] >= 0 && !over ? len[of[i]] : 0;
+        o.base = of[i] >= 0 ? len[of[i]] : 0;
         o.group = o.base > 0 ? of[i] : -1;
         o.ctx = s[i].ctx;
         o.len = positions(a, s[i]);
@@ -202,10 +195,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
         o.units = max(1, units_of(o.len - o.base));
         rows[2 * i + 1] = blocks_of(o.rows, lrb);
         o.big = rows[2 * i + 1].big;
-        atomicAdd(&cost[1], (unsigned long long)cost_of(o, rows[2 * i + 1]));
+        atomicAdd(&cost, (unsigned long long)cost_of(o, rows[2 * i + 1]));
     }
     __syncthreads();
-    const int64_t goal = prefix_goal((int64_t)((over ? 0 : cost[0]) + cost[1]));
+    const int64_t goal = prefix_goal((int64_t)cost);
     const int length[2] = {prefix_full(goal, kUnitCost), prefix_full(goal, small_cost)};
     const float scale = (float)kBuckets / (float)goal;
     Two count{0, 0}, first, all;  // full pieces of the groups, of the sequences
