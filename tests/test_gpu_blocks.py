@@ -192,6 +192,23 @@ def test_choice_of_many_blocks(blocks, count, tokens):
     select_and_check(q, bounds_of(5000, 1, 64, F16, g), table, [0, tokens], [blocks * 16 + 5], count, 16, *((2, 3) if count > 5 else (0, 0)))
 
 
+@pytest.mark.parametrize("kv,tokens,seqs", [(32, 1, 33), (8, 16, 9), (64, 2, 8)], ids=str)
+def test_choice_for_many_rows(kv, tokens, seqs):
+    """Short contexts of many tokens and heads, up to and beyond 128 blocks; equal scores, NaN and blocks on no page."""
+    g = gen(kv)
+    bounds = bounds_of(40, kv, 64, F16, g)
+    bounds[7, 0, 0, 3] = bounds[7, 0, 1, 3] = math.nan
+    start = [tokens * b for b in range(seqs + 1)]
+    q = randn((seqs * tokens, kv, 64), F16, g)
+    for cols in (63, 128, 129):
+        table = torch.randint(-1, 41, (seqs, cols), dtype=torch.int32, device=DEV, generator=g)
+        ctx = [min((b * 47) % 140, cols) * 16 + b % 16 for b in range(seqs)]
+        for count, first, last in ((1, 0, 0), (20, 1, 2), (60, 30, 30)):
+            select_and_check(q, bounds, table, start, ctx, count, 16, first, last)
+            if count == 20:
+                select_and_check(q, bounds, table, start, ctx, count, 16, first, last, tree=max(1, tokens - 1), max_len=max(ctx))
+
+
 @pytest.mark.parametrize("tokens", [1, 17])
 @pytest.mark.parametrize("blocks", [100, 600, 5000])
 def test_equal_scores_go_to_the_lowest_index(blocks, tokens):

@@ -10,7 +10,8 @@
 // summing (in 32 bits blocks next to the border would change sides with it), and the vector unit does them at the
 // rate of 32 bits. Where lo or hi is infinite and its factor 0 the right side is no number, though the left one may be:
 // scores that are NaN are taken again without the products with 0.
-// k_select: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits.
+// k_select, k_select_few: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits or
+// by ranks.
 #include "cache_internal.h"
 
 namespace ubw {
@@ -19,6 +20,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(4))) int32_t ScalarWord;
 __device__ inline int scalar_word(const int32_t* p, int64_t i) { return ((ScalarWord*)(uintptr_t)p)[i]; }
@@ -84,6 +86,65 @@ struct Elems<UBW_E4M3> {
 };
 
 // ---- bounds
+// The smallest and the largest of each of a lane's 16 bytes of elements. A NaN stays one.
+template <int DT>
+struct Range {
+    using E = Elems<DT>;
+    float lo[E::N], hi[E::N];
+    __device__ void add(u32x4 w, bool first) {
+        float x[E::N];
+        E::read(w, x);
+#pragma unroll
+        for (int e = 0; e < E::N; ++e) {
+            lo[e] = first ? x[e] : __builtin_elementwise_minimum(lo[e], x[e]);
+            hi[e] = first ? x[e] : __builtin_elementwise_maximum(hi[e], x[e]);
+        }
+    }
+    __device__ void write(char* to, int apart) const {
+        *reinterpret_cast<u32x4*>(to) = E::write(lo);
+        *reinterpret_cast<u32x4*>(to + apart) = E::write(hi);
+    }
+};
+// 8 bits, as whole numbers: with the other seven bits turned where the sign is set they ascend as the numbers do, the
+// NaN below and above all others. Bytes are compared in the upper halves of 16 bits, the even ones moved there: 8
+// instructions for four, where numbers of 32 bits take 10 (new pages of 36 sequences, 32 heads, 28 layers: 147 MB of 128
+// dims 30 us instead of 31, of 256 dims 58 instead of 63).
+template <>
+struct Range<UBW_E4M3> {
+    s16x2 lo[8], hi[8];
+    static __device__ uint32_t turned(uint32_t w) {
+        return w ^ (__builtin_amdgcn_perm(w, w << 8, 0x0b090a08u) & 0x7f7f7f7fu);  // (the signs, over their bytes)
+    }
+    static __device__ uint32_t zero_bytes(uint32_t w) { return ~(((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w | 0x7f7f7f7fu); }
+    __device__ void add(u32x4 w, bool first) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t t = turned(w[i]);
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+                const s16x2 x = __builtin_bit_cast(s16x2, odd ? t : t << 8);
+                lo[2 * i + odd] = first ? x : __builtin_elementwise_min(lo[2 * i + odd], x);
+                hi[2 * i + odd] = first ? x : __builtin_elementwise_max(hi[2 * i + odd], x);
+            }
+        }
+    }
+    static __device__ uint32_t joined(s16x2 even, s16x2 odd) {
+        return (__builtin_bit_cast(uint32_t, even) >> 8 & 0x00ff00ffu) | (__builtin_bit_cast(uint32_t, odd) & 0xff00ff00u);
+    }
+    __device__ void write(char* to, int apart) const {
+        u32x4 l, h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = joined(lo[2 * i], lo[2 * i + 1]), y = joined(hi[2 * i], hi[2 * i + 1]);
+            const uint32_t nan = ((zero_bytes(x ^ 0x80808080u) | zero_bytes(y ^ 0x7f7f7f7fu)) >> 7) * 0xffu;
+            l[i] = (turned(x) & ~nan) | (nan & 0x7f7f7f7fu);
+            h[i] = (turned(y) & ~nan) | (nan & 0x7f7f7f7fu);
+        }
+        *reinterpret_cast<u32x4*>(to) = l;
+        *reinterpret_cast<u32x4*>(to + apart) = h;
+    }
+};
+
 // As many lanes as a row has 16 bytes go through a page of one head together, each with its own dims, several rows
 // requested at once: no lane needs another's.
 template <int DT, int D>
@@ -101,7 +162,7 @@ __global__ __launch_bounds__(256) void k_bounds(BoundsArgs a) {
         const int page = a.table[b * a.ld_table + first + col];
         if ((uint32_t)page >= (uint32_t)a.c.pages) continue;
         const char* k = a.c.k + layer * a.c.k_layer + page * a.c.k_page + h * a.c.k_head + lane * 16;
-        float lo[E::N], hi[E::N];
+        Range<DT> range;
         u32x4 w[2 * AHEAD];
 #pragma unroll
         for (int i = 0; i < 2 * AHEAD; ++i) w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + (int64_t)i * a.c.k_row));
@@ -118,19 +179,10 @@ __global__ __launch_bounds__(256) void k_bounds(BoundsArgs a) {
                     w[AHEAD + i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(k + (int64_t)(r0 + 2 * AHEAD + i) * a.c.k_row));
             }
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                float x[E::N];
-                E::read(now[i], x);
-#pragma unroll
-                for (int e = 0; e < E::N; ++e) {  // (a NaN stays one)
-                    lo[e] = r0 + i == 0 ? x[e] : __builtin_elementwise_minimum(lo[e], x[e]);
-                    hi[e] = r0 + i == 0 ? x[e] : __builtin_elementwise_maximum(hi[e], x[e]);
-                }
-            }
+            for (int i = 0; i < AHEAD; ++i) range.add(now[i], r0 + i == 0);
         }
         char* to = static_cast<char*>(a.bounds) + (((int64_t)layer * a.c.pages + page) * a.c.heads + h) * (2 * D * E::kSize) + lane * 16;
-        *reinterpret_cast<u32x4*>(to) = E::write(lo);
-        *reinterpret_cast<u32x4*>(to + D * E::kSize) = E::write(hi);
+        range.write(to, D * E::kSize);
     }
 }
 
@@ -164,24 +216,30 @@ __device__ inline void up_down(const SelectArgs& a, int token, int h, int d, int
     *up = u;
     *down = v;
 }
-// The same of eight dims, whose rows are requested together.
-template <typename TQ>
-__device__ inline void up_down8(const SelectArgs& a, int token, int h, int d, int dims, double* up, double* down) {
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)token * a.ldq + (int64_t)h * a.group * dims + d;
-    for (int g0 = 0; g0 < a.group; g0 += 8) {
-        u32x4 w[8];
+// The same of eight dims; N heads' rows are requested together, those behind the last are zeros.
+template <typename TQ, int N>
+__device__ inline void add_heads(const uint16_t* q, int heads, int dims, double (&up)[8], double (&down)[8]) {
+    u32x4 w[N];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) w[g] = *reinterpret_cast<const u32x4*>(q + (int64_t)min(g0 + g, a.group - 1) * dims);
+    for (int g = 0; g < N; ++g) w[g] = *reinterpret_cast<const u32x4*>(q + (int64_t)min(g, heads - 1) * dims);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            if (g0 + g >= a.group) break;
+    for (int g = 0; g < N; ++g) {
+        if (g >= heads) w[g] = u32x4{};  // (without a branch, which would keep the loads apart)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = number<TQ>((uint16_t)(w[g][e >> 1] >> (16 * (e & 1))));
-                up[e] += __builtin_elementwise_maximum(x, 0.0f);  // (a NaN in both)
-                down[e] += __builtin_elementwise_minimum(x, 0.0f);
-            }
+        for (int e = 0; e < 8; ++e) {
+            const float x = number<TQ>((uint16_t)(w[g][e >> 1] >> (16 * (e & 1))));
+            up[e] += __builtin_elementwise_maximum(x, 0.0f);  // (a NaN in both)
+            down[e] += __builtin_elementwise_minimum(x, 0.0f);
         }
+    }
+}
+template <typename TQ>
+__device__ inline void up_down8(const SelectArgs& a, int token, int h, int d, int dims, double (&up)[8], double (&down)[8]) {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)token * a.ldq + (int64_t)h * a.group * dims + d;
+    if (a.group == 1) return add_heads<TQ, 1>(q, 1, dims, up, down);
+    for (int g = 0; g < a.group; g += 8) {
+        if (a.group - g > 4) add_heads<TQ, 8>(q + (int64_t)g * dims, a.group - g, dims, up, down);
+        else add_heads<TQ, 4>(q + (int64_t)g * dims, a.group - g, dims, up, down);
     }
 }
 // Scores as whole numbers of the same order: a NaN is the largest, both zeros are one, 0 is below all.
@@ -285,89 +343,88 @@ __global__ __launch_bounds__(256) void k_scores(SelectArgs a) {
     }
 }
 
-// Trees: 16 blocks x 16 tokens a product of the matrix cores, in 64 bits. A workgroup takes kScoreBlocksTree blocks.
+// Trees: 16 blocks x 16 tokens a product of the matrix cores, in 64 bits. A workgroup takes kScoreBlocksTree blocks of
+// 16 tokens, its waves two times 16 blocks in turn.
 // Lane (c, j) holds of block c the 16-byte pieces j, j + 4, ..; the tokens' sums lie in LDS in the order of the
 // products' lanes.
 template <int DT, typename TQ, int D>
-__global__ __launch_bounds__(256) void k_scores_tree(SelectArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 2 : 1) void k_scores_tree(SelectArgs a) {
     using E = Elems<DT>;
     constexpr int S = D / (4 * E::N), TILES = kScoreBlocksTree / 64;
     __shared__ double q[2][S * E::N][64];
-    const int b = blockIdx.y, h = blockIdx.x % a.kv, c0 = blockIdx.x / a.kv * kScoreBlocksTree;
+    const int b = blockIdx.y, h = blockIdx.x % a.kv, c0 = blockIdx.x / a.kv * kScoreBlocksTree, t0 = blockIdx.z * 16;
     const Rows s = rows_of(a, b);
-    if (s.n <= 0 || c0 >= s.whole || s.whole <= a.count) return;
+    if (t0 >= s.n || c0 >= s.whole || s.whole <= a.count) return;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, j = lane >> 4;
-    for (int t0 = 0; t0 < s.n; t0 += 16) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * D; i += 256) {  // eight dims of a token
-            const int t = i / (D / 8), d = i % (D / 8) * 8, piece = d / E::N;
-            double u[8] = {}, v[8] = {};
-            if (t0 + t < s.n) up_down8<TQ>(a, s.q0 + t0 + t, h, d, D, u, v);
+    for (int i = threadIdx.x; i < 2 * D; i += 256) {  // eight dims of a token
+        const int t = i / (D / 8), d = i % (D / 8) * 8, piece = d / E::N;
+        double u[8] = {}, v[8] = {};
+        if (t0 + t < s.n) up_down8<TQ>(a, s.q0 + t0 + t, h, d, D, u, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int at = piece / 4 * E::N + (d + e) % E::N, to = piece % 4 * 16 + t;
-                q[0][at][to] = v[e];
-                q[1][at][to] = u[e];
-            }
+        for (int e = 0; e < 8; ++e) {
+            const int at = piece / 4 * E::N + (d + e) % E::N, to = piece % 4 * 16 + t;
+            q[0][at][to] = v[e];
+            q[1][at][to] = u[e];
         }
-        __syncthreads();
-        for (int i = 0; i < TILES; i += 2) {  // two tiles at a time share the tokens' sums
-            const int first = c0 + (wave * TILES + i) * 16;
-            if (first >= s.whole) break;
-            int page[2];
-            const char* at[2];
+    }
+    __syncthreads();
+    const auto put = [&](f64x4 score, int page, int first) {
+        const uint64_t all = __ballot(page >= 0);
+        if (t0 + c >= s.n) return;
+        uint64_t* keys = a.keys + ((int64_t)(s.q0 + t0 + c) * a.kv + h) * a.stride + first;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int x = first + 16 * k + c;
-                page[k] = x < s.whole ? a.table[b * a.ld_table + x] : -1;
-                if ((uint32_t)page[k] >= (uint32_t)a.pages) page[k] = -1;
-                at[k] = static_cast<const char*>(a.bounds) + ((int64_t)max(page[k], 0) * a.kv + h) * (2 * D * E::kSize) + j * 16;
-            }
-            f64x4 sum[2][2] = {};  // of each tile, lower and upper bounds
-            u32x4 w[2][2][S];
+        for (int r = 0; r < 4; ++r) {
+            const int x = 4 * r + j;
+            double y = score[r];
+            if (first + x >= s.whole) continue;
+            if (y != y && (all >> x) & 1)
+                y = without_zeros<DT, D>(a, a.table[b * a.ld_table + first + x], h, [&](int half, int d) {
+                    return q[half][d / E::N / 4 * E::N + d % E::N][d / E::N % 4 * 16 + c];
+                });
+            keys[x] = (all >> x) & 1 ? key_of(y) : 0;
+        }
+    };
+#pragma unroll 1
+    for (int i = 0; i < TILES; i += 2) {  // two tiles at a time share the tokens' sums
+        const int first = c0 + (4 * i + 2 * wave) * 16;
+        if (first >= s.whole) break;
+        int page[2];
+        const char* at[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int x = first + 16 * k + c;
+            page[k] = x < s.whole ? a.table[b * a.ld_table + x] : -1;
+            if ((uint32_t)page[k] >= (uint32_t)a.pages) page[k] = -1;
+            at[k] = static_cast<const char*>(a.bounds) + ((int64_t)max(page[k], 0) * a.kv + h) * (2 * D * E::kSize) + j * 16;
+        }
+        f64x4 sum[2][2] = {};  // of each tile, lower and upper bounds
+        u32x4 w[2][2][S];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int n = 0; n < S; ++n) w[k][x][n] = *reinterpret_cast<const u32x4*>(at[k] + x * D * E::kSize + n * 64);
+#pragma unroll
+        for (int n = 0; n < S; ++n) {
+            float y[2][2][E::N];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 2; ++x) E::read(w[k][x][n], y[k][x]);
 #pragma unroll
-                    for (int n = 0; n < S; ++n) w[k][x][n] = *reinterpret_cast<const u32x4*>(at[k] + x * D * E::kSize + n * 64);
+            for (int e = 0; e < E::N; ++e)
 #pragma unroll
-            for (int n = 0; n < S; ++n) {
-                float y[2][2][E::N];
+                for (int x = 0; x < 2; ++x) {
+                    const double t = q[x][n * E::N + e][lane];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) E::read(w[k][x][n], y[k][x]);
-#pragma unroll
-                for (int e = 0; e < E::N; ++e)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const double t = q[x][n * E::N + e][lane];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            sum[k][x] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)y[k][x][e], t, sum[k][x], 0, 0, 0);
-                    }
-            }
-            // lane (t, j) has the blocks j, j + 4, .. of token t
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint64_t all = __ballot(page[k] >= 0);
-                if (t0 + c < s.n) {
-                    uint64_t* keys = a.keys + ((int64_t)(s.q0 + t0 + c) * a.kv + h) * a.stride + first + 16 * k;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int x = 4 * r + j;
-                        if (first + 16 * k + x >= s.whole) continue;
-                        double score = sum[k][0][r] + sum[k][1][r];
-                        if (score != score && (all >> x) & 1)
-                            score = without_zeros<DT, D>(a, a.table[b * a.ld_table + first + 16 * k + x], h, [&](int half, int d) {
-                                return q[half][d / E::N / 4 * E::N + d % E::N][d / E::N % 4 * 16 + c];
-                            });
-                        keys[x] = (all >> x) & 1 ? key_of(score) : 0;
-                    }
+                    for (int k = 0; k < 2; ++k)
+                        sum[k][x] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)y[k][x][e], t, sum[k][x], 0, 0, 0);
                 }
-            }
         }
+        // lane (t, j) has the blocks j, j + 4, .. of token t
+        put(sum[0][0] + sum[0][1], page[0], first);
+        put(sum[1][0] + sum[1][1], page[1], first + 16);
     }
 }
 
@@ -594,6 +651,49 @@ __global__ __launch_bounds__(kSelThreads) void k_select(SelectArgs a) {
     }
 }
 
+// Up to kFewBlocks blocks and kManyRows (token, head) or more: a wave has one of these to itself and ranks each of its
+// keys among all. (22 trees of 1 to 38 tokens, 4 heads, 90 blocks: with the scores 26.8 us, by k_select 32.1; 42 tokens, 32
+// heads, 49 to 97 blocks 16.1 and 16.5; one of these tokens 11.9 and 9.7, as four waves rank sooner than one.)
+constexpr int kFewBlocks = 128, kManyRows = 1024;
+__global__ __launch_bounds__(256) void k_select_few(SelectArgs a) {
+    constexpr int R = kFewBlocks / 64;
+    const int lane = threadIdx.x & 63, b = blockIdx.y, x = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    const int i = x / a.kv, h = x - i * a.kv;
+    const Rows s = rows_of(a, b);
+    if (i >= s.n) return;
+    const int64_t row = (int64_t)(s.q0 + i) * a.kv + h;
+    int32_t* out = a.blocks + row * a.count;
+    if (s.whole <= a.count) {
+        for (int k = lane; k < a.count; k += 64) out[k] = k < s.whole ? k : -1;
+        return;
+    }
+    for (int k = lane; k < a.first; k += 64) out[k] = k;
+    for (int k = lane; k < a.last; k += 64) out[a.count - a.last + k] = s.whole - a.last + k;
+    const int m = s.whole - a.first - a.last, need = a.count - a.first - a.last;
+    const uint64_t* keys = a.keys + row * a.stride + a.first;
+    uint64_t mine[R];
+    int rank[R] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r) mine[r] = r * 64 + lane < m ? keys[r * 64 + lane] : 0;
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+#pragma unroll 4
+        for (int j = 0; j < min(m - q * 64, 64); ++j) {
+            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)mine[q], j), hi = __builtin_amdgcn_readlane((int)(mine[q] >> 32), j);
+            const uint64_t k = (uint64_t)hi << 32 | lo;
+#pragma unroll
+            for (int r = 0; r < R; ++r) rank[r] += q < r ? k >= mine[r] : q > r ? k > mine[r] : k > mine[r] || (k == mine[r] && j < lane);
+        }
+    int before = a.first;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool in = r * 64 + lane < m && rank[r] < need;
+        const uint64_t all = __ballot(in);
+        if (in) out[before + __popcll(all & ((1ull << lane) - 1))] = a.first + r * 64 + lane;
+        before += __popcll(all);
+    }
+}
+
 template <int DT, int D>
 hipError_t bounds_d(const BoundsArgs& a, int64_t pages, hipStream_t s) {
     constexpr int kGroups = 256 / (D * Elems<DT>::kSize / 16);
@@ -610,8 +710,12 @@ hipError_t select_d(const SelectArgs& a, hipStream_t s) {
     if (a.max_tree == 1)
         k_scores<DT, TQ, D><<<dim3((unsigned)(cdiv(a.stride, kScoreBlocks) * a.kv), (unsigned)a.batch), 256, 0, s>>>(a);
     else
-        k_scores_tree<DT, TQ, D><<<dim3((unsigned)(cdiv(a.stride, kScoreBlocksTree) * a.kv), (unsigned)a.batch), 256, 0, s>>>(a);
-    k_select<<<dim3((unsigned)(a.max_tree * a.kv), (unsigned)a.batch), kSelThreads, 0, s>>>(a);
+        k_scores_tree<DT, TQ, D><<<dim3((unsigned)(cdiv(a.stride, kScoreBlocksTree) * a.kv), (unsigned)a.batch, (unsigned)cdiv(a.max_tree, 16)), 256, 0, s>>>(a);
+    const int64_t rows = (int64_t)a.max_tree * a.kv;
+    if (a.stride <= kFewBlocks && rows * a.batch >= kManyRows)
+        k_select_few<<<dim3((unsigned)cdiv(rows, 4), (unsigned)a.batch), 256, 0, s>>>(a);
+    else
+        k_select<<<dim3((unsigned)rows, (unsigned)a.batch), kSelThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int DT, typename TQ>
