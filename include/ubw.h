@@ -539,7 +539,9 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
  * positions are read by its own row, and so are the last up to 15 of a prefix that is no multiple of 16, and
  * all positions of a sequence in no group. A prefix_len that passes the shortest context of the group's
  * sequences (those that have tokens) counts as that context, one below 0 as 0. Results are those of
- * ubw_tree_attn, up to the order of summing.
+ * ubw_tree_attn, up to the order of summing. (Short contexts, batch times max_len or table_cols * page_size positions of up
+ * to 96 MiB of keys and values, are read by each sequence's own row, which then takes less time.)
+ *   max_len      as there; it also says what counts as short
  *   group_start  int32 [groups + 1] ascending, prefix_len int32 [groups]; groups at most UBW_MAX_SEQS
  *                (0: both may be NULL)
  *   workspace    ubw_prefix_attn_workspace_bytes() bytes, for as many tokens as the call has or more; always

@@ -47,8 +47,16 @@ def shared_batch(first, prefix, own, drafts, page, kv, dim, dtype, g, token_majo
     return cache, torch.from_numpy(table).to(DEV), ctx
 
 
-def call(q, cache, table, start, ctx, first, prefix, masks=None, tree=None, ws=None, scale=None, **kw):
+def wide_of(table, cache):
+    """The table with columns on no page, so many that contexts could be long ones: short ones are not shared."""
+    position = 2 * cache.kv_heads * cache.head_dim * cache.k.element_size()
+    cols = (100 << 20) // (position * table.shape[0] * cache.page_size) + 1
+    return torch.nn.functional.pad(table, (0, max(cols - table.shape[1], 0)), value=-1)
+
+
+def call(q, cache, table, start, ctx, first, prefix, masks=None, tree=None, ws=None, scale=None, wide=True, **kw):
     t, heads, dim = q.shape
+    table = wide_of(table, cache) if wide else table
     tree = tree or max(1, max(b - a for a, b in zip(start, start[1:])))
     if ws is None:
         ws = ubw.prefix_attn_workspace(len(ctx), len(prefix), t, tree, heads, cache.kv_heads, dim, DEV)
@@ -83,8 +91,11 @@ def test_every_tile(qt, ct, dim, rows):
     masks = random_masks(start[-1], g)
     masks[start[10]] = 0   # no context, no mask: sees nothing
     got = call(q, cache, table, start, ctx, first, prefix, masks)
-    check_attention(*got, attention_reference(q, cache, table, start, ctx, masks), qt, 500)
-    again = call(q, cache, table, start, ctx, first, prefix, masks, max_len=max(c + n for c, n in zip(ctx, drafts)))
+    want = attention_reference(q, cache, table, start, ctx, masks)
+    check_attention(*got, want, qt, 500)
+    short = call(q, cache, table, start, ctx, first, prefix, masks, max_len=max(c + n for c, n in zip(ctx, drafts)))
+    check_attention(*short, want, qt, 500)   # (that short, nothing is shared)
+    again = call(q, cache, table, start, ctx, first, prefix, masks)
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
@@ -196,6 +207,7 @@ def test_what_is_out_of_range():
     check_attention(out[:6], lse[:6], tuple(x[:6] for x in want), F16, cols * page)
     ws = ubw.prefix_attn_workspace(4, 5, 7, 3, heads, kv, dim, DEV)
     guard = torch.full((ws.numel() + 64,), 7.0, device=DEV)
+    table = wide_of(table, cache)
     for groups in ([0, 4, 0, 4, 0, 4], [4, 3, 2, 1, 0, 0], [-5, 9, 2, 3, 100, 2 ** 31 - 1], [0, 0, 0, 0, 0, 4]):
         for starts in ([0, 2, 4, 6, 7], [5, -3, 1000, 2, 7], [7, 0, 7, 0, 7]):
             guard.fill_(7.0)
@@ -283,6 +295,7 @@ def test_streams_graphs_and_devices():
     want = call(q, cache, table, start, ctx, first, prefix)
     ws = [ubw.prefix_attn_workspace(6, 2, 25, 16, heads, kv, dim, DEV) for _ in "abc"]
     args = [i32(x) for x in (start, ctx, first, prefix)]
+    table = wide_of(table, cache)
     streams, outs = [torch.cuda.Stream() for _ in "ab"], [torch.zeros_like(q) for _ in "ab"]
     torch.cuda.synchronize()
     for _ in range(10):
@@ -307,6 +320,28 @@ def test_streams_graphs_and_devices():
         eager = ubw.prefix_attn(q, cache, table, *args, max_tree=16, workspace=ws[0])
         torch.cuda.synchronize()
         assert torch.equal(out, eager), lens
+
+
+@pytest.mark.parametrize("qt,ct,heads,kv,dim", [(F16, F16, 16, 2, 128), (BF16, E4M3, 8, 8, 64), (F16, E4M3, 24, 2, 256)], ids=str)
+def test_short_contexts_are_those_of_tree_attention(qt, ct, heads, kv, dim):
+    """... bit by bit; where the caller says that they are short, too, and up to the order of summing where not."""
+    g = gen(23)
+    first, prefix, own, drafts = [0, 3, 6], [700, 250], [100, 0, 30, 5, 60, 7, 9], [4, 1, 2, 16, 1, 0, 1]
+    cache, table, ctx = shared_batch(first, prefix, own, drafts, 32, kv, dim, ct, g)
+    start = [0] + list(np.cumsum(drafts))
+    q = randn((25, heads, dim), qt, g)
+    masks = random_masks(25, g)
+    out, lse = torch.full_like(q, 77.0), torch.full((25, heads), 77.0, device=DEV)
+    ws = ubw.tree_attn_workspace(7, 16, heads, kv, dim, DEV)
+    ubw.tree_attn(q, cache, table, i32(start), i32(ctx), masks, max_tree=16, out=out, lse=lse, workspace=ws)
+    want = attention_reference(q, cache, table, start, ctx, masks)
+    check_attention(out, lse, want, qt, 900)
+    got = call(q, cache, table, start, ctx, first, prefix, masks, wide=False)
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    ubw.tree_attn(q, cache, wide_of(table, cache), i32(start), i32(ctx), masks, max_tree=16, max_len=820, out=out, lse=lse, workspace=ws)
+    got = call(q, cache, table, start, ctx, first, prefix, masks, max_len=820)
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    check_attention(*call(q, cache, table, start, ctx, first, prefix, masks), want, qt, 900)
 
 
 def test_arguments():

@@ -10,6 +10,10 @@ A decoding step of a batch, for one layer:
 and once per step, for all layers: pages_reserve before it, cache_compact (of the drafted tokens that
 were accepted) and pages_trim behind it.
 
+Sequences that pages_fork made share the beginning of their contexts; prefix_attn in place of tree_attn reads it once
+for all of them. Long contexts need not be read whole: page_bounds after each step that fills pages (for all layers),
+then per layer block_select, which names the blocks that matter to each token, and block_attn over these.
+
 KVCache and PagePool hold the tensors and their descriptors, checked once; the calls check what
 changes from call to call. Every call runs on its tensors' device, on that device's current stream.
 """
@@ -232,8 +236,9 @@ def prefix_attn(q, cache, table, q_start, ctx_len, group_start, prefix_len, mask
     """tree_attn for sequences that have the beginning of their contexts in common: the sequences group_start[g] ..
     group_start[g + 1] - 1 (int32 [groups + 1], ascending) hold the same keys and values at the first prefix_len[g]
     (int32 [groups]) positions, which are read once for all of them, by the table row of the first sequence that has
-    tokens. Sequences in no group have their contexts for themselves. workspace: prefix_attn_workspace(); the other
-    arguments as tree_attn's."""
+    tokens. Sequences in no group have their contexts for themselves, and so has a batch of short ones, where that takes
+    less time (max_len, or else the table's width, tells). workspace: prefix_attn_workspace(); the other arguments as
+    tree_attn's."""
     out, first, last = _attn_args(q, cache, table, q_start, ctx_len, masks, scale, out, lse)
     i32, dev = torch.int32, cache.index
     groups = prefix_len.numel()

@@ -7,6 +7,11 @@
 //
 // Pieces are numbered head by head, then by the run of positions, tokens side by side: those of one tree, which
 // share most of their blocks, run at the same time on one XCD and meet in its L2.
+//
+// Bound: single tokens of a batch the memory (64 ragged contexts, 64 blocks of 32 positions each, bf16: 86 us, 5.9
+// TB/s), one token alone the chain list -> table -> keys -> values -> join (9.6 and 4.1 us, 13.1 in a queue), trees the issue of a
+// step, whose 16-row tile a token of 8 query heads fills by half (8 trees of 16 over 64 blocks of 64 positions in 8 bits
+// 95 us, 11 TB/s out of the L2).
 #include "attn_pieces.h"
 
 namespace ubw {

@@ -143,6 +143,23 @@ int ubw_tree_attn_workspace_bytes(int batch, int max_tree, int heads, int kv_hea
     return UBW_OK;
 }
 
+namespace {
+// Positions that a sequence has at most, as the table or the caller says.
+int64_t longest_of(const AttnArgs& a, int64_t max_len) {
+    const int64_t room = (int64_t)a.table_cols << a.c.lps;
+    return max_len > 0 && max_len < room ? max_len : room;
+}
+int run_attn(AttnArgs& a, int cache_dtype, int q_dtype, int d, int64_t max_len, void* stream) {
+    const int64_t rows = (int64_t)a.max_tree * a.group;
+    const AttnTile t = attn_tile(rows, d);
+    a.max_items = attn_max_items(a.batch, rows, a.c.heads, d, t);
+    if (a.max_items > kMaxGrid) return UBW_ERANGE;
+    // short contexts are not split: one launch
+    a.target = a.ws && longest_of(a, max_len) > attn_unsplit(t, d, (int64_t)a.batch * a.c.heads) ? attn_target(t, d) : 0;
+    return hip_status(launch_attn(a, cache_dtype, q_dtype, d, t, as_stream(stream)));
+}
+}  // namespace
+
 int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t ldq, int64_t tokens, int heads,
                   const int32_t* q_start, const int32_t* ctx_len, int batch, const int32_t* table, int64_t ld_table,
                   int table_cols, int max_tree, int64_t max_len, const uint64_t* masks, float scale, void* out,
@@ -156,15 +173,8 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
     if ((st = ubw_tree_attn_workspace_bytes(batch, max_tree, heads, a.c.heads, d, &need)) != UBW_OK ||
         (st = check_workspace(workspace, ws_bytes, need, true)) != UBW_OK)
         return st;
-    const int64_t rows = (int64_t)max_tree * a.group;
-    const AttnTile t = attn_tile(rows, d);
-    if (attn_max_items(batch, rows, a.c.heads, d, t) > kMaxGrid) return UBW_ERANGE;
     a.ws = static_cast<float*>(workspace);
-    a.max_items = attn_max_items(batch, rows, a.c.heads, d, t);
-    // short contexts (as the table or the caller says) are not split: one launch
-    const int64_t room = (int64_t)table_cols << a.c.lps, longest = max_len > 0 && max_len < room ? max_len : room;
-    a.target = workspace && longest > attn_unsplit(t, d, (int64_t)batch * a.c.heads) ? attn_target(t, d) : 0;
-    return hip_status(launch_attn(a, cache->dtype, q_dtype, d, t, as_stream(stream)));
+    return run_attn(a, cache->dtype, q_dtype, d, max_len, stream);
 }
 
 int ubw_prefix_attn_workspace_bytes(int batch, int groups, int64_t tokens, int max_tree, int heads, int kv_heads,
@@ -195,12 +205,14 @@ int ubw_prefix_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64
     if ((st = ubw_prefix_attn_workspace_bytes(batch, groups, tokens, max_tree, heads, a.c.heads, d, &need)) != UBW_OK ||
         (st = check_workspace(workspace, ws_bytes, need, false)) != UBW_OK)
         return st;
+    a.ws = static_cast<float*>(workspace);
+    const int64_t position_bytes = 2 * (int64_t)a.c.heads * d * type_size(cache->dtype);
+    if (prefix_alone(batch, longest_of(a, max_len), position_bytes)) return run_attn(a, cache->dtype, q_dtype, d, max_len, stream);
     const PrefixSizes z = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * a.group, a.group, a.c.heads, d);
     if (z.lists > kMaxGrid) return UBW_ERANGE;
     a.group_start = group_start;
     a.prefix_len = prefix_len;
     a.groups = groups;
-    a.ws = static_cast<float*>(workspace);
     a.plan = reinterpret_cast<int*>(a.ws + z.rows * prefix_row_floats(d));
     return hip_status(launch_prefix_attn(a, cache->dtype, q_dtype, d, as_stream(stream)));
 }

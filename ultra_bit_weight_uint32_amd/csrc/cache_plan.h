@@ -220,8 +220,20 @@ inline PrefixSizes prefix_sizes(int batch, int groups, int64_t tokens, int64_t m
 inline int64_t prefix_row_floats(int head_dim) { return head_dim + 4; }
 inline int64_t prefix_workspace_floats(int batch, int groups, int64_t tokens, int max_tree, int group, int kv_heads, int head_dim) {
     const PrefixSizes p = prefix_sizes(batch, groups, tokens, (int64_t)max_tree * group, group, kv_heads, head_dim);
-    return p.rows * prefix_row_floats(head_dim) + p.words;
+    const int64_t alone = attn_workspace_floats(batch, max_tree, group, kv_heads, head_dim);
+    const int64_t x = p.rows * prefix_row_floats(head_dim) + p.words;
+    return x > alone ? x : alone;
 }
+// Where all sequences' contexts, each as long as the longest may be, are up to 96 MiB of keys and values, tree attention
+// goes through them: it has one launch or two, not three. Times in us, tree attention / shared; one group, 60 positions
+// behind the prefix, 64 heads over 8 of 128 dims, 16 bits, single tokens unless stated:
+//   4 sequences of 250 positions (5 MB) 10.9 / 21.7, of 1000 (17) 17.8 / 22.0, of 4000 (67) 24.4 / 27.2, of 16000 (263) 54.7 / 47.8
+//   64 of 250 (82) 14.2 / 33.2; 16 of 1000 (70) 26.5 / 25.9, of 4000 (266) 54.7 / 34.7, of 4000 in 8 bits (133) 34.5 / 33.7
+//   trees of 8: 4 of 4000 (67) 36.2 / 43.0, 16 of 1000 (70) 38.2 / 38.3, of 4000 (267) 63.5 / 56.6
+//   32 heads over 32: 4 of 1000 (70) 27.1 / 24.1, 2 of 4000 (133) 31.7 / 33.1, 4 of 4000 (266) 53.1 / 33.4
+//   16 heads over 2 of 256 dims: 16 of 1000 (35) 21.1 / 23.4, 4 of 16000 (132) 34.7 / 30.4
+constexpr int64_t kPrefixLeast = (int64_t)96 << 20;
+inline bool prefix_alone(int64_t batch, int64_t longest, int64_t position_bytes) { return batch * longest <= kPrefixLeast / position_bytes; }
 
 // ---- selected blocks ------------------------------------------------------------------------
 // Attention over them: a token and key/value head have their rows (the head's queries) and positions to
