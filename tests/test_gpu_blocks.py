@@ -501,6 +501,7 @@ def test_a_decoding_loop(dtype):
             ubw.tree_attn(q, cache, *args, max_tree=tree, out=dense, lse=dense_lse)
             # both within half a step of fp16 and their weights' roundings (2^-11 each) of a mean of values below 6
             assert (all_out.float() - dense.float()).abs().max() <= 4 * 2.0 ** -11 * 6
+            # the same scores, up to 400 weights summed in fp32 in another order: 2 (400 + 64) V + 8 V (|lse| + 16) < 1e-4, V = 2^-24
             assert (all_lse - dense_lse).abs().max() <= 1e-4
         after = [a + n for a, n in zip(length, new)]
         ubw.pages_trim(pool, i32(after))
