@@ -209,6 +209,19 @@ def test_choice_for_many_rows(kv, tokens, seqs):
                 select_and_check(q, bounds, table, start, ctx, count, 16, first, last, tree=max(1, tokens - 1), max_len=max(ctx))
 
 
+@pytest.mark.parametrize("cols", [256, 257, 512, 513, 1024, 1025])
+def test_choice_for_many_rows_of_longer_contexts(cols):
+    """8 trees of 16 tokens, 32 heads: two contexts of the whole table and nearly so, the others short."""
+    g = gen(cols)
+    bounds = bounds_of(60, 32, 64, F16, g)
+    bounds[7, 0, 0, 3] = bounds[7, 0, 1, 3] = math.nan
+    table = torch.randint(-1, 61, (8, cols), dtype=torch.int32, device=DEV, generator=g)
+    ctx = [cols * 16, 30, 0, (cols - 70) * 16 + 3, 500, 16 * 16, 16 * 17, 2 ** 31 - 1 if cols < 500 else 7]
+    q = randn((128, 32, 64), F16, g)
+    for count, first, last in ((16, 1, 2), (70, 0, 0)):
+        select_and_check(q, bounds, table, [16 * b for b in range(9)], ctx, count, 16, first, last)
+
+
 @pytest.mark.parametrize("tokens", [1, 17])
 @pytest.mark.parametrize("blocks", [100, 600, 5000])
 def test_equal_scores_go_to_the_lowest_index(blocks, tokens):

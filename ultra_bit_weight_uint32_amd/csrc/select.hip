@@ -10,8 +10,7 @@
 // summing (in 32 bits blocks next to the border would change sides with it), and the vector unit does them at the
 // rate of 32 bits. Where lo or hi is infinite and its factor 0 the right side is no number, though the left one may be:
 // scores that are NaN are taken again without the products with 0.
-// k_select, k_select_few: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits or
-// by ranks.
+// k_select, k_select_few: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits.
 #include "cache_internal.h"
 
 namespace ubw {
@@ -655,12 +654,14 @@ __global__ __launch_bounds__(kSelThreads) void k_select(SelectArgs a) {
     }
 }
 
-// Up to kFewBlocks blocks and kManyRows (token, head) or more: a wave has one of these to itself and ranks each of its
-// keys among all. (22 trees of 1 to 38 tokens, 4 heads, 90 blocks: with the scores 26.8 us, by k_select 32.1; 42 tokens, 32
-// heads, 49 to 97 blocks 16.1 and 16.5; one of these tokens 11.9 and 9.7, as four waves rank sooner than one.)
-constexpr int kFewBlocks = 128, kManyRows = 1024;
+// Up to 64 R blocks: a wave has a token and head to itself, and finds the need-th key bit by bit, without a barrier. With
+// the scores, in us, by this / by k_select; 8 heads, one token, 64 tokens and 64 trees of 16:
+//   60 blocks 6.9 / 10.1, 8.7 / 12.3, 27 / 70; 250 blocks 7.9 / 10.3, 19.2 / 21.9, 43 / 83
+//   500 blocks 9.6 / 10.3, 30.3 / 30.9, 68 / 104; 1000 blocks 12.7 / 10.5, 52.5 / 50.0, 128 / 157
+// so that more than kFewBlocks take it only if there are kManyRows (token, head).
+constexpr int kFewBlocks = 512, kManyBlocks = 1024, kManyRows = 4096;
+template <int R>
 __global__ __launch_bounds__(256) void k_select_few(SelectArgs a) {
-    constexpr int R = kFewBlocks / 64;
     const int lane = threadIdx.x & 63, b = blockIdx.y, x = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     const int i = x / a.kv, h = x - i * a.kv;
     const Rows s = rows_of(a, b);
@@ -675,25 +676,32 @@ __global__ __launch_bounds__(256) void k_select_few(SelectArgs a) {
     for (int k = lane; k < a.last; k += 64) out[a.count - a.last + k] = s.whole - a.last + k;
     const int m = s.whole - a.first - a.last, need = a.count - a.first - a.last;
     const uint64_t* keys = a.keys + row * a.stride + a.first;
+    if (need <= 0) return;
     uint64_t mine[R];
-    int rank[R] = {};
 #pragma unroll
     for (int r = 0; r < R; ++r) mine[r] = r * 64 + lane < m ? keys[r * 64 + lane] : 0;
+    uint64_t last = 0;  // the largest number that `need` keys reach
+    for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t k = last | 1ull << bit;
+        int count = 0;
 #pragma unroll
-    for (int q = 0; q < R; ++q)
-#pragma unroll 4
-        for (int j = 0; j < min(m - q * 64, 64); ++j) {
-            const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)mine[q], j), hi = __builtin_amdgcn_readlane((int)(mine[q] >> 32), j);
-            const uint64_t k = (uint64_t)hi << 32 | lo;
+        for (int r = 0; r < R; ++r) count += __popcll(__ballot(mine[r] >= k));
+        if (count >= need) last = k;
+        if (count == need) break;  // these are they
+    }
+    int equal = need;  // of those with this key: the first ones
 #pragma unroll
-            for (int r = 0; r < R; ++r) rank[r] += q < r ? k >= mine[r] : q > r ? k > mine[r] : k > mine[r] || (k == mine[r] && j < lane);
-        }
-    int before = a.first;
+    for (int r = 0; r < R; ++r) equal -= __popcll(__ballot(mine[r] > last));
+    const uint64_t below = (1ull << lane) - 1;
+    int before = a.first, seen = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const bool in = r * 64 + lane < m && rank[r] < need;
+        const bool is = r * 64 + lane < m && mine[r] == last;
+        const uint64_t same = __ballot(is);
+        const bool in = mine[r] > last || (is && seen + __popcll(same & below) < equal);
         const uint64_t all = __ballot(in);
-        if (in) out[before + __popcll(all & ((1ull << lane) - 1))] = a.first + r * 64 + lane;
+        if (in) out[before + __popcll(all & below)] = a.first + r * 64 + lane;
+        seen += __popcll(same);
         before += __popcll(all);
     }
 }
@@ -716,10 +724,12 @@ hipError_t select_d(const SelectArgs& a, hipStream_t s) {
     else
         k_scores_tree<DT, TQ, D><<<dim3((unsigned)(cdiv(a.stride, kScoreBlocksTree) * a.kv), (unsigned)a.batch, (unsigned)cdiv(a.max_tree, 16)), 256, 0, s>>>(a);
     const int64_t rows = (int64_t)a.max_tree * a.kv;
-    if (a.stride <= kFewBlocks && rows * a.batch >= kManyRows)
-        k_select_few<<<dim3((unsigned)cdiv(rows, 4), (unsigned)a.batch), 256, 0, s>>>(a);
-    else
-        k_select<<<dim3((unsigned)rows, (unsigned)a.batch), kSelThreads, 0, s>>>(a);
+    const dim3 few((unsigned)cdiv(rows, 4), (unsigned)a.batch);
+    if (a.stride <= 128) k_select_few<2><<<few, 256, 0, s>>>(a);
+    else if (a.stride <= 256) k_select_few<4><<<few, 256, 0, s>>>(a);
+    else if (a.stride <= kFewBlocks) k_select_few<8><<<few, 256, 0, s>>>(a);
+    else if (a.stride <= kManyBlocks && rows * a.batch >= kManyRows) k_select_few<16><<<few, 256, 0, s>>>(a);
+    else k_select<<<dim3((unsigned)rows, (unsigned)a.batch), kSelThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int DT, typename TQ>
