@@ -178,7 +178,7 @@ inline int64_t attn_workspace_floats(int batch, int max_tree, int group, int kv_
 // number of rows, with the small tile 1.5; single tokens behind one of 16K in 16 bits: 4.5 and 2.6; 8 to 10 us to begin
 // and end a piece): every one of 512 workgroups is to have the same. So lists are cut into full pieces, one to a
 // workgroup, as long as that allows, and a rest; the workgroups without a full piece share out the rests, the longest
-// first, in runs of the same cost.
+// first, in runs of the same cost. (Where these would have too much the full pieces are made longer.)
 constexpr int kPrefixWgs = 512;  // two on every CU
 constexpr int kUnitCost = 7, kSmallUnitCost = 4, kSmallUnitCost8 = 3, kPieceCost = 16;  // in 0.64 us; 8: 8-bit caches
 constexpr int kSmallRows = 32;

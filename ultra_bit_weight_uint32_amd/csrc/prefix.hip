@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 static_assert(kPlanThreads >= kPrefixWgs, "a thread for every workgroup of rests");
+constexpr int kTurns = 6;     // at cutting the lists
 constexpr int kBuckets = 64;  // rests are sorted by their length in 64ths of a full piece
 
 // An owner in the plan. Class 0: whole blocks of rows, class 1: the small one.
@@ -206,49 +207,63 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
     }
     __syncthreads();
     const int64_t goal = prefix_goal((int64_t)cost);
-    const int length[2] = {prefix_full(goal, kUnitCost), prefix_full(goal, small_cost)};
     const float scale = (float)kBuckets / (float)goal;
-    Two count{0, 0}, first, all;  // full pieces of the groups, of the sequences
+    Two first, all;          // full pieces of the groups, of the sequences
     int in[2 * EACH][2];     // places in the rests' buckets
     const auto bucket_of = [&](int rest, int c) {  // the longest first
         return kBuckets - 1 - min((int)((float)rest * (float)(c ? small_cost : kUnitCost) * scale), kBuckets - 1);
     };
     // What a rest of bucket b costs.
     const auto each_of = [&](int b) { return ((float)(kBuckets - b) - 0.5f) / scale + (float)kPieceCost; };
+    int64_t full_cost = goal;
+    for (int turn = 0;; ++turn) {
+        const int length[2] = {prefix_full(full_cost, kUnitCost), prefix_full(full_cost, small_cost)};
+        Two count{0, 0};
 #pragma unroll
-    for (int i = 0; i < 2 * EACH; ++i) {
+        for (int i = 0; i < 2 * EACH; ++i) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int lists = (c ? rows[i].small : rows[i].big) * kv;
-            const PrefixCut cut = prefix_cut(x[i].units, length[c]);
-            x[i].full[c] = lists > 0 ? cut.full : 0;
-            x[i].rest[c] = lists > 0 ? cut.rest : 0;
-            (i & 1 ? count.b : count.a) += x[i].full[c] * lists;
-            if (x[i].rest[c] > 0) in[i][c] = atomicAdd(&bucket[bucket_of(x[i].rest[c], c)], lists);
+            for (int c = 0; c < 2; ++c) {
+                const int lists = (c ? rows[i].small : rows[i].big) * kv;
+                const PrefixCut cut = prefix_cut(x[i].units, length[c]);
+                x[i].full[c] = lists > 0 ? cut.full : 0;
+                x[i].rest[c] = lists > 0 ? cut.rest : 0;
+                (i & 1 ? count.b : count.a) += x[i].full[c] * lists;
+                if (x[i].rest[c] > 0) in[i][c] = atomicAdd(&bucket[bucket_of(x[i].rest[c], c)], lists);
+            }
         }
+        first = plan_before(count, lds, &all);  // (the buckets are full, too)
+        if (tid < kBuckets) {
+            int y = bucket[tid];
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int z = __shfl_up(y, d);
+                if (tid >= d) y += z;
+            }
+            float z = (float)bucket[tid] * each_of(tid);
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const float u = __shfl_up(z, d);
+                if (tid >= d) z += u;
+            }
+            bucket0[tid + 1] = y;
+            cost0[tid + 1] = z;
+            if (tid == 0) bucket0[0] = 0, cost0[0] = 0.f;
+            if (tid == kBuckets - 1) {
+                at.head[0] = all.a + all.b;
+            }
+        }
+        __syncthreads();
+        // Lengths are whole units, so that full pieces can be more, or leave fewer workgroups to the rests, than they
+        // were to: longer ones then (64 single tokens behind six prefixes of 6K to 12K positions, one head of 256 dims, three
+        // units a piece: 64 rests on 8 workgroups 120 us, with longer pieces 55).
+        const int full = all.a + all.b;
+        const bool fits = full <= kPrefixWgs && cost0[kBuckets] <= 1.25f * (float)full_cost * (float)rest_bins(full);
+        if (fits || turn == kTurns - 1) break;
+        __syncthreads();
+        full_cost += max((int64_t)kUnitCost, (full_cost - kPieceCost) / 8);
+        if (tid < kBuckets) bucket[tid] = 0;
+        __syncthreads();
     }
-    first = plan_before(count, lds, &all);  // (the buckets are full, too)
-    if (tid < kBuckets) {
-        int y = bucket[tid];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int z = __shfl_up(y, d);
-            if (tid >= d) y += z;
-        }
-        float z = (float)bucket[tid] * each_of(tid);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const float u = __shfl_up(z, d);
-            if (tid >= d) z += u;
-        }
-        bucket0[tid + 1] = y;
-        cost0[tid + 1] = z;
-        if (tid == 0) bucket0[0] = 0, cost0[0] = 0.f;
-        if (tid == kBuckets - 1) {
-            at.head[0] = all.a + all.b;
-        }
-    }
-    __syncthreads();
     first.b += all.a;
 #pragma unroll
     for (int i = 0; i < 2 * EACH; ++i) {
