@@ -165,6 +165,42 @@ def test_batches_larger_than_a_workgroup(seqs, groups, kv, group, longest):
     assert not (out == 77).any()
 
 
+@pytest.mark.parametrize("kv,ct,kinds", [(10, E4M3, [(8, 39, 32), (8, 20, 62), (8, 4, 31)]), (4, E4M3, [(8, 92, 54), (8, 36, 64), (4, 2, 215)]),
+                                         (10, E4M3, [(8, 47, 44), (8, 11, 66), (8, 22, 23)]), (10, E4M3, [(8, 18, 61), (8, 60, 37), (8, 100, 44)]),
+                                         (4, BF16, [(4, 74, 100), (8, 4, 64), (8, 18, 111)])], ids=str)
+def test_batches_of_a_few_lengths(kv, ct, kinds):
+    """Batches of two or three lengths (tokens, units of 128 positions, sequences): many rests of one cost, dealt out where
+    the beginnings of several workgroups' runs fall together (computed by each workgroup in 32 bits, the last three left lists
+    out). Every row is written, near tree attention's; some are held against 64 bits."""
+    g = gen(kv + kinds[0][1])
+    group, dim, page = 5, 128, 64
+    r = np.random.default_rng(kv)
+    each = [(n, u) for n, u, seqs in kinds for _ in range(seqs)]
+    each = [each[i] for i in r.permutation(len(each))]
+    most = max(u for _, u in each)
+    ctx = [128 * u - n - int(r.integers(0, 128 - n)) for n, u in each]
+    start = [0] + list(np.cumsum([n for n, _ in each]))
+    cache = cache_of(300, kv, page, dim, ct, g)   # sequences have pages in common here and there
+    table = torch.randint(0, 300, (len(ctx), 2 * most), dtype=torch.int32, device=DEV, generator=g)
+    q = randn((int(start[-1]), kv * group, dim), BF16, g)
+    out, lse = call(q, cache, table, start, ctx, [0], [], wide=False)
+    whole, whole_lse = torch.empty_like(q), torch.empty_like(lse)
+    ubw.tree_attn(q, cache, table, i32(start), i32(ctx), max_tree=8, out=whole, lse=whole_lse)
+    # each is within 2 half steps (2^-8) of its mean of values, and a little; values are multiplied by less than 1.5
+    assert (out.float() - whole.float()).abs().max() <= 2.0 ** -6 * 1.5 * cache.v.float().abs().max()
+    # sums in fp32 over up to 128 `most` positions: relatively within (positions + 64) 2^-24 of the exact ones, each score
+    # within (dim + 20) 2^-24 of scale sum |q||k| < 64, and the logarithm 4 2^-24 (|lse| + 16)
+    assert (lse - whole_lse).abs().max() <= 2 * 2.0 ** -24 * (128 * most + 64 + 148 * 64 + 4 * 80)
+    for b in r.integers(0, len(ctx), 3):
+        rows = slice(start[b], start[b + 1])
+        for h in (0, kv * group - 1):
+            hk = h // group
+            one = ubw.KVCache(cache.k[:, hk:hk + 1].contiguous(), cache.v[:, hk:hk + 1].contiguous(),
+                              *(None if s is None else s[hk:hk + 1].clone() for s in (cache.k_scale, cache.v_scale)))
+            want = attention_reference(q[rows, h:h + 1], one, table[b:b + 1], [0, each[b][0]], [ctx[b]], None)
+            check_attention(out[rows, h:h + 1], lse[rows, h:h + 1], want, BF16, 128 * most)
+
+
 @pytest.mark.parametrize("kv,group,dim,qt,ct", [(2, 8, 128, BF16, BF16), (1, 3, 64, F16, F16), (2, 8, 128, BF16, E4M3),
                                                 (1, 4, 256, F16, F16), (2, 1, 128, F16, E4M3)], ids=str)
 def test_long_prefixes(kv, group, dim, qt, ct):

@@ -201,6 +201,106 @@ UBW_HD inline PrefixCut prefix_cut(int units, int length) {
 // Full pieces: a list of u units has at most u / length of them, and length >= (goal - kPieceCost) / (2 unit_cost), so
 // that they are at most 2 cost / (cost / 512).
 constexpr int kPrefixFull = 2 * kPrefixWgs;
+// The rests lie in buckets by what they cost, the dearest first. Costs and rooms are whole numbers, in 2^-16 of a goal, at
+// most 2^17 for a rest and 2^41 for all: no sum of them depends on the order of summing, so that every workgroup finds
+// its run's beginning by the same sums as the next one finds its end. (In 32 bits, each workgroup's rounded its own way, a run
+// could begin one rest before the end of the one before it, whose workgroup then left out one of its long rests.)
+constexpr int kRestBuckets = 64;
+UBW_HD inline int rest_bucket(int rest, int unit_cost, float scale) {  // scale: kRestBuckets / goal
+    const int x = (int)((float)rest * (float)unit_cost * scale);
+    return kRestBuckets - 1 - (x < kRestBuckets - 1 ? x : kRestBuckets - 1);
+}
+UBW_HD inline int64_t rest_begin_cost(int64_t goal) { return ((int64_t)kPieceCost << 16) / goal; }  // (goal >= kPieceCost)
+// What a rest of bucket b costs: the middle of the bucket, and to begin and end it.
+UBW_HD inline int64_t rest_cost(int b, int64_t begin) { return (2 * (kRestBuckets - b) - 1) * ((int64_t)1 << 16) / (2 * kRestBuckets) + begin; }
+// Workgroups for the rests: each XCD's that have no full piece (all, if it has as many full pieces as workgroups).
+UBW_HD inline int rest_bins(int full) {
+    const int per = (full + 7) >> 3;
+    return per < kPrefixWgs / 8 ? kPrefixWgs - 8 * per : kPrefixWgs;
+}
+// Lengths are whole units, so that full pieces can be more than workgroups, or leave fewer of them to the rests, which
+// cost `rests` in all, than they were to: longer ones then (64 single tokens behind six prefixes of 6K to 12K positions, one
+// head of 256 dims, three units a piece: 64 rests on 8 workgroups 120 us, with longer pieces 55).
+constexpr int kPrefixTurns = 6;
+UBW_HD inline bool prefix_fits(int full, int64_t rests, int64_t goal, int64_t full_cost) {
+    return full <= kPrefixWgs && (float)rests * (float)goal <= 1.25f * 65536.f * (float)full_cost * (float)rest_bins(full);
+}
+UBW_HD inline int64_t prefix_longer(int64_t full_cost) {
+    const int64_t more = (full_cost - kPieceCost) / 8;
+    return full_cost + (more > kUnitCost ? more : kUnitCost);
+}
+// Long rests, of more than a quarter of what such a workgroup is to have, go there and back over them; the others, in
+// order, fill up what those leave free. The buckets of long ones:
+UBW_HD inline int long_buckets(int64_t have, int64_t begin) {
+    int lo = 0, hi = kRestBuckets;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (4 * rest_cost(mid, begin) > have) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+}
+// The n-th of the long rests that the w-th of the workgroups has: there and back.
+UBW_HD inline int rest_at(int n, int w, int bins) { return n * bins + (n & 1 ? bins - 1 - w : w); }
+// What the long ones leave free of the w-th. before: rests in the buckets before each one.
+UBW_HD inline int64_t rest_room(int w, int bins, int longs, int64_t have, const int* before, int64_t begin) {
+    int64_t room = have;
+    for (int n = 0;; ++n) {
+        const int k = rest_at(n, w, bins);
+        if (k >= longs) break;
+        int from = 0, end = kRestBuckets;  // its bucket: the last that begins at k or before
+        while (end - from > 1) {
+            const int mid = (from + end) >> 1;
+            if (before[mid] <= k) from = mid; else end = mid;
+        }
+        room -= rest_cost(from, begin);
+    }
+    return room > 0 ? room : 0;
+}
+// The first of the other rests of the workgroup that has `room` of `rooms` before it. before, cost: rests in the buckets
+// before each one, and what they cost; longs: buckets of long ones. Where room ascends it does not descend: whole
+// numbers of this size are doubles, a quotient, a product and a sum with the same numbers, however they are rounded,
+// turn no order around, and a bucket's rests are all behind those of the one before it.
+UBW_HD inline int rest_run(int64_t room, int64_t rooms, const int* before, const int64_t* cost, int longs, int64_t begin) {
+    if (longs == kRestBuckets) return before[kRestBuckets];
+    const double left = (double)(cost[kRestBuckets] - cost[longs]);
+    const double from = (double)cost[longs] + (rooms > 0 ? (double)room / (double)rooms * left : 0.0);
+    int b = longs, end = kRestBuckets;
+    while (end - b > 1) {
+        const int mid = (b + end) >> 1;
+        if ((double)cost[mid] <= from) b = mid; else end = mid;
+    }
+    const int n = before[b + 1] - before[b];
+    const double k = (from - (double)cost[b]) / (double)rest_cost(b, begin);  // (from >= cost[longs])
+    const int up = (int)(k < (double)n ? k : (double)n);
+    return before[b] + (up < n && (double)up < k ? up + 1 : up);
+}
+// What workgroup wg has of `full` full pieces, `longs` long rests and the others, which begin at run[w] for the w-th
+// workgroup with rests. Each XCD has an eighth of the full pieces, in order.
+struct PrefixShare {
+    int full0, fulls;  // full pieces full0, full0 + kPrefixWgs / 8, ..
+    int bin, bins;     // among the workgroups with rests
+    int longs;         // long rests
+    int rest0, rests;  // others
+};
+template <typename Run>
+UBW_HD inline PrefixShare prefix_share(int wg, int full, int longs, Run run) {
+    const int xcd = wg & 7, i = wg >> 3, per = (full + 7) >> 3, wide = kPrefixWgs / 8;
+    const int left = full - xcd * per, mine = left < per ? left : per, taken = per < wide ? per : 0;
+    PrefixShare s{xcd * per + i, i < mine ? (mine - i + wide - 1) / wide : 0, (i - taken) * 8 + xcd, rest_bins(full), 0, 0, 0};
+    if (i >= taken) {
+        s.rest0 = run[s.bin];
+        s.rests = run[s.bin + 1] - s.rest0;
+        while (rest_at(s.longs, s.bin, s.bins) < longs) ++s.longs;
+    }
+    return s;
+}
+// Its n-th piece, in the plan's list (the full ones, then the rests at kPrefixFull); -1 behind the last.
+UBW_HD inline int prefix_work(const PrefixShare& s, int n) {
+    if (n < s.fulls) return s.full0 + n * (kPrefixWgs / 8);
+    const int k = n - s.fulls;
+    if (k >= s.longs + s.rests) return -1;
+    return kPrefixFull + (k < s.longs ? rest_at(k, s.bin, s.bins) : s.rest0 + k - s.longs);
+}
 // The workspace: sums of the full pieces (head_dim means, maximum, sum, two unused words a row), of the rests of each
 // (token, head) over the own positions and over the prefix; the plan: a head, sixteen words an owner, two words a piece.
 constexpr int kPlanHead = 16 + kPrefixWgs, kPlanOwner = 16;

@@ -27,8 +27,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 static_assert(kPlanThreads >= kPrefixWgs, "a thread for every workgroup of rests");
-constexpr int kTurns = 6;     // at cutting the lists
-constexpr int kBuckets = 64;  // rests are sorted by their length in 64ths of a full piece
+static_assert(kRestBuckets == 64, "a lane for every bucket");
 
 // An owner in the plan. Class 0: whole blocks of rows, class 1: the small one.
 struct Owner {
@@ -90,13 +89,16 @@ __device__ inline Two plan_before(Two mine, Two (&lds)[kPlanThreads / 64], Two* 
     return x;
 }
 
-// Workgroups for the rests: each XCD's that have no full piece (all, if it has as many full pieces as workgroups).
-__device__ inline int rest_bins(int full) {
-    const int per = (full + 7) >> 3;
-    return per < kPrefixWgs / 8 ? kPrefixWgs - 8 * per : kPrefixWgs;
+// The sum of x over the lanes up to this one.
+template <typename N>
+__device__ inline N lanes_up_to(N x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const N u = __shfl_up(x, d);
+        if ((int)(threadIdx.x & 63) >= d) x += u;
+    }
+    return x;
 }
-// The n-th of the long rests that the w-th of these has: there and back.
-__device__ inline int rest_at(int n, int w, int bins) { return n * bins + (n & 1 ? bins - 1 - w : w); }
 // Blocks of `rows` rows: whole ones, and a small one. (The tile of 256 dims has no small one.)
 struct RowBlocks {
     int big, small;
@@ -111,12 +113,12 @@ template <int EACH>
 __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, int small_cost) {
     constexpr int kMost = EACH * kPlanThreads;
     __shared__ int start[kMost + 1], len[kMost], lead[kMost], last[kMost];
-    __shared__ int bucket[kBuckets], bucket0[kBuckets + 1];     // rests, and those before
-    __shared__ float cost0[kBuckets + 1];                       // what those before cost
-    __shared__ unsigned long long cost;                         // of all lists
+    __shared__ int bucket[kRestBuckets], bucket0[kRestBuckets + 1];  // rests, and those before
+    __shared__ int64_t cost0[kRestBuckets + 1];                      // what those before cost
+    __shared__ unsigned long long cost;                              // of all lists
     __shared__ int full0[4 * kMost];  // first full piece of each owner's classes
     __shared__ Two lds[kPlanThreads / 64];
-    __shared__ float rooms[kPlanThreads / 64];
+    __shared__ int64_t rooms[kPlanThreads / 64];
     const int tid = threadIdx.x, kv = a.c.heads;
     const PlanAt at = plan_at(a.plan, a.groups + a.batch);
     const int most = (int)min((int64_t)a.table_cols << a.c.lps, (int64_t)1 << 30);
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
             last[g] = -1;
         }
     }
-    if (tid < kBuckets) bucket[tid] = 0;
+    if (tid < kRestBuckets) bucket[tid] = 0;
     if (tid == 0) cost = 0;
     Seq s[EACH];
     int of[EACH];
@@ -207,14 +209,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
     }
     __syncthreads();
     const int64_t goal = prefix_goal((int64_t)cost);
-    const float scale = (float)kBuckets / (float)goal;
+    const float scale = (float)kRestBuckets / (float)goal;
+    const int64_t begin = rest_begin_cost(goal);
     Two first, all;          // full pieces of the groups, of the sequences
     int in[2 * EACH][2];     // places in the rests' buckets
-    const auto bucket_of = [&](int rest, int c) {  // the longest first
-        return kBuckets - 1 - min((int)((float)rest * (float)(c ? small_cost : kUnitCost) * scale), kBuckets - 1);
-    };
-    // What a rest of bucket b costs.
-    const auto each_of = [&](int b) { return ((float)(kBuckets - b) - 0.5f) / scale + (float)kPieceCost; };
+    const auto bucket_of = [&](int rest, int c) { return rest_bucket(rest, c ? small_cost : kUnitCost, scale); };
     int64_t full_cost = goal;
     for (int turn = 0;; ++turn) {
         const int length[2] = {prefix_full(full_cost, kUnitCost), prefix_full(full_cost, small_cost)};
@@ -232,36 +231,19 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
             }
         }
         first = plan_before(count, lds, &all);  // (the buckets are full, too)
-        if (tid < kBuckets) {
-            int y = bucket[tid];
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int z = __shfl_up(y, d);
-                if (tid >= d) y += z;
-            }
-            float z = (float)bucket[tid] * each_of(tid);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const float u = __shfl_up(z, d);
-                if (tid >= d) z += u;
-            }
+        if (tid < kRestBuckets) {
+            const int y = lanes_up_to(bucket[tid]);
+            const int64_t z = lanes_up_to((int64_t)bucket[tid] * rest_cost(tid, begin));
             bucket0[tid + 1] = y;
             cost0[tid + 1] = z;
-            if (tid == 0) bucket0[0] = 0, cost0[0] = 0.f;
-            if (tid == kBuckets - 1) {
-                at.head[0] = all.a + all.b;
-            }
+            if (tid == 0) bucket0[0] = 0, cost0[0] = 0;
+            if (tid == kRestBuckets - 1) at.head[0] = all.a + all.b;
         }
         __syncthreads();
-        // Lengths are whole units, so that full pieces can be more, or leave fewer workgroups to the rests, than they
-        // were to: longer ones then (64 single tokens behind six prefixes of 6K to 12K positions, one head of 256 dims, three
-        // units a piece: 64 rests on 8 workgroups 120 us, with longer pieces 55).
-        const int full = all.a + all.b;
-        const bool fits = full <= kPrefixWgs && cost0[kBuckets] <= 1.25f * (float)full_cost * (float)rest_bins(full);
-        if (fits || turn == kTurns - 1) break;
+        if (prefix_fits(all.a + all.b, cost0[kRestBuckets], goal, full_cost) || turn == kPrefixTurns - 1) break;
         __syncthreads();
-        full_cost += max((int64_t)kUnitCost, (full_cost - kPieceCost) / 8);
-        if (tid < kBuckets) bucket[tid] = 0;
+        full_cost = prefix_longer(full_cost);
+        if (tid < kRestBuckets) bucket[tid] = 0;
         __syncthreads();
     }
     first.b += all.a;
@@ -293,61 +275,22 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan(PrefixArgs a, int lrb, in
         }
         at.full[k] = Work{lo >> 1, (lo & 1) << 30 | (k - full0[lo])};
     }
-    // The rests for the workgroups without a full piece. Long ones, of more than a quarter of what such a workgroup is to have, go
-    // there and back over them; the others, in order, fill up what those leave free.
-    const int bins = rest_bins(all.a + all.b), rests = bucket0[kBuckets];
-    const float have = cost0[kBuckets] / (float)bins;
-    int lo = 0, hi = kBuckets;  // buckets of long ones
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (each_of(mid) > 0.25f * have) lo = mid + 1; else hi = mid;
-    }
-    const int longs = bucket0[lo], long_buckets = lo;
-    float room = 0.f;
-    if (tid < bins) {
-        room = have;
-        for (int n = 0;; ++n) {
-            const int k = rest_at(n, tid, bins);
-            if (k >= longs) break;
-            int from = 0, end = kBuckets;  // its bucket: the last that begins at k or before
-            while (end - from > 1) {
-                const int mid = (from + end) >> 1;
-                if (bucket0[mid] <= k) from = mid; else end = mid;
-            }
-            room -= each_of(from);
-        }
-        room = fmaxf(room, 0.f);
-    }
-    float y = room;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const float u = __shfl_up(y, d);
-        if ((tid & 63) >= d) y += u;
-    }
+    // The rests for the workgroups without a full piece.
+    const int bins = rest_bins(all.a + all.b), rests = bucket0[kRestBuckets];
+    const int64_t have = cost0[kRestBuckets] / bins;
+    const int long_ones = long_buckets(have, begin), longs = bucket0[long_ones];
+    const int64_t room = tid < bins ? rest_room(tid, bins, longs, have, bucket0, begin) : 0;
+    const int64_t y = lanes_up_to(room);
     if ((tid & 63) == 63) rooms[tid >> 6] = y;
     __syncthreads();
-    float before = y - room, total = 0.f;
+    int64_t before = y - room, total = 0;
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 64; ++w) {
         if (w < (tid >> 6)) before += rooms[w];
         total += rooms[w];
     }
-    if (tid < bins) {
-        const float left = cost0[kBuckets] - cost0[long_buckets];
-        const float from = cost0[long_buckets] + (total > 0.f ? fminf(before / total, 1.f) * left : 0.f);
-        int b = long_buckets, end = kBuckets;
-        while (end - b > 1) {
-            const int mid = (b + end) >> 1;
-            if (cost0[mid] <= from) b = mid; else end = mid;
-        }
-        int k = longs;
-        if (b < kBuckets) {
-            const int n = bucket0[b + 1] - bucket0[b];
-            k = bucket0[b] + (n > 0 ? min(max((int)ceilf((from - cost0[b]) / each_of(b)), 0), n) : 0);
-        }
-        at.run[tid] = tid == 0 ? longs : max(k, longs);
-        if (tid == 0) at.run[bins] = rests;
-    }
+    if (tid < bins) at.run[tid] = rest_run(before, total, bucket0, cost0, long_ones, begin);
+    if (tid == 0) at.run[bins] = rests;
     if (tid == 0) at.head[1] = longs;
 }
 
@@ -372,29 +315,13 @@ __global__ __launch_bounds__(256, 2) void k_prefix(PrefixArgs a) {
     __shared__ __align__(1024) SharedOf<typename W::Big, typename W::Small> sh;
     const PlanAt at = plan_at(a.plan, a.groups + a.batch);
     const int full = scalar_words(at.head)[0];
-    // Workgroup (xcd, i) has the full pieces i, i + 64, .. of its XCD's eighth; those without one have the rests.
-    const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3, per = (full + 7) >> 3, wide = kPrefixWgs / 8;
-    const int mine = min(per, full - xcd * per), fulls = i < mine ? (mine - i + wide - 1) / wide : 0;
-    const int taken = per < wide ? per : 0, bin = (i - taken) * 8 + xcd;
-    const int bins = rest_bins(full), longs = scalar_words(at.head)[1];
-    int rest0 = 0, rests = 0, mine_long = 0;
-    if (i >= taken) {
-        rest0 = scalar_words(at.run)[bin];
-        rests = scalar_words(at.run)[bin + 1] - rest0;
-        while (rest_at(mine_long, bin, bins) < longs) ++mine_long;
-    }
+    const PrefixShare share = prefix_share(blockIdx.x, full, scalar_words(at.head)[1], scalar_words(at.run));
     // Work n of this workgroup, -1 behind the last.
     Work work{0, 0};
     const auto get = [&](int n) {
-        const Work* from;
-        if (n < fulls) {
-            from = at.full + xcd * per + i + n * wide;
-        } else {
-            const int k = n - fulls;
-            if (k >= mine_long + rests) return -1;
-            from = at.rest + (k < mine_long ? rest_at(k, bin, bins) : rest0 + k - mine_long);
-        }
-        const ScalarWord* w = scalar_words(reinterpret_cast<const int*>(from));
+        const int k = prefix_work(share, n);
+        if (k < 0) return -1;
+        const ScalarWord* w = scalar_words(reinterpret_cast<const int*>(at.full + k));
         work = Work{w[0], w[1]};
         return n;
     };
