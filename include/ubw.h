@@ -540,7 +540,8 @@ int ubw_tree_attn(const ubw_kv_cache* cache, const void* q, int q_dtype, int64_t
  * all positions of a sequence in no group. A prefix_len that passes the shortest context of the group's
  * sequences (those that have tokens) counts as that context, one below 0 as 0. Results are those of
  * ubw_tree_attn, up to the order of summing. (Short contexts, batch times max_len or table_cols * page_size positions of up
- * to 96 MiB of keys and values, are read by each sequence's own row, which then takes less time.)
+ * to 96 MiB of keys and values, are read by each sequence's own row, which then takes less time. What longer ones share is
+ * known on the device alone: where nothing, or next to nothing, is shared, ubw_tree_attn takes less.)
  *   max_len      as there; it also says what counts as short
  *   group_start  int32 [groups + 1] ascending, prefix_len int32 [groups]; groups at most UBW_MAX_SEQS
  *                (0: both may be NULL)
@@ -585,11 +586,11 @@ int ubw_page_bounds(const ubw_kv_cache* cache, void* bounds, const int32_t* tabl
  * block with bounds lo, hi is
  *   sum over h's query heads g and dims d of max(q[t][g][d] lo[d], q[t][g][d] hi[d])
  * (an element of q that is 0 adds nothing, whatever the bounds), summed in 64 bits: no sum over g of q[t][g] . k for a
- * key k of the block is larger. The first `first` and the last `last` whole blocks are always chosen, then those of the
+ * key k of the block is larger, and scores that differ by more than the last bits of such a sum are told apart. The first `first` and the last `last` whole blocks are always chosen, then those of the
  * largest scores (a NaN counts as the largest; equal ones: the lowest index first). Contexts of `count` whole blocks or
  * fewer have all of them chosen.
  *   bounds   of one layer, [pages][kv_heads][2][head_dim] of type dtype, as ubw_page_bounds leaves them. (k_scale, one
- *            factor for all blocks of a head, does not change the choice.)
+ *            positive factor for all blocks of a head, does not change the choice.)
  *   q        q_dtype (UBW_F16 or UBW_BF16; dtype unless that is UBW_E4M3), rows as in ubw_tree_attn
  *   q_start, ctx_len, table, max_tree  as in ubw_tree_attn. A block on no valid page is chosen last.
  *   max_len  the largest context (with or without the tokens behind it); 0: unknown. Blocks beyond it are not looked at.

@@ -17,6 +17,9 @@
 //     keys are widened as well, or (bf16 queries, 128 dims or more) multiplied as they are by queries in
 //     two 8-bit parts, which costs the matrix cores the same and the vector unit nothing: 4 trees of 64 tokens
 //     over 30K to 65K positions (512 rows of a head) 520 -> 455 us.
+//     Weights of 16 bits are what the matrix cores take at this rate beside 16-bit values; rounded to nearest, each is off by
+//     half a step of the type (fp16 2^-11, bf16 2^-8) at most, as the output is once more, while l sums them unrounded
+//     (relative to 64 bits bf16 outputs are off by 0.0023, with weights of 32 bits by 0.0017; fp16 by 0.00025 and 0.00021).
 //   * m is not followed exactly: o is scaled only when a score passes m by more than 2^8 (a wave-uniform
 //     branch that long contexts take a few times), so the usual step has no cross-lane work at all, l is
 //     kept per lane, and fp16 weights p = 2^((s - m) log2 e + 7) stay below 2^15, inside fp16, while those down

@@ -15,10 +15,12 @@
 //
 // Bound: behind many rows the loop's issue and latency (a unit of 128 positions takes 4.0 to 4.5 us with 128 rows or
 // fewer, 2 workgroups a CU), behind few rows the memory, and 8 to 10 us to begin and end a piece. 64 samples over a prompt of
-// 16K positions, 64 heads over 8 of 128 dims, bf16: plan 10, pieces 86, join 8 us, 102 in a queue (two launches for the
-// two parts 147; tree attention, which reads the prompt 64 times, 697); five groups of trees in 8 bits 13, 230, 20 and
-// 233 (0.68 PFLOP/s; 388); 40 sequences of 32 heads with keys of their own 11, 85, 5 and 102 (4.2 TB/s; 636). Short
-// contexts are left to tree attention (prefix_alone).
+// 16K positions, 64 heads over 8 of 128 dims, bf16: plan 11, pieces 86 to 89 (matrix cores busy 24% of the cycles, the vector
+// unit 34%), join 8 us, 102 to 104 in a queue (tree attention, which reads the prompt 64 times, 697); five groups of trees in
+// 8 bits 14, 225 to 239 one launch at a time (39% and 52%), 20 and 234 in a queue (0.68 PFLOP/s; 388); 40 sequences of 32
+// heads with keys of their own 11, 85, 5 and 102 (4.2 TB/s; 636). Short contexts are left to tree attention (prefix_alone).
+// More than 1024 sequences or groups: k_plan keeps part of its eight owners a thread in scratch (1500 sequences 31 us, 4096 in
+// four groups 49, in 4096 groups 61; 512 sequences 11, 1024 15).
 #include "attn_pieces.h"
 
 namespace ubw {

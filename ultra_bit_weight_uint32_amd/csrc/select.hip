@@ -6,9 +6,10 @@
 //     sum over h's query heads g and dims d of max(q_gd lo_d, q_gd hi_d) = sum_d hi_d up_d + lo_d down_d,
 //     up_d = sum_g max(q_gd, 0),  down_d = sum_g min(q_gd, 0),
 // which no sum over g of q_g k for a key k of the block passes. The right side costs 2 D products a block, however
-// many query heads there are. Sums are 64 bits wide: the choice then depends on the values alone, not on the order of
-// summing (in 32 bits blocks next to the border would change sides with it), and the vector unit does them at the
-// rate of 32 bits. Where lo or hi is infinite and its factor 0 the right side is no number, though the left one may be:
+// many query heads there are. Sums are 64 bits wide: in 32 bits the order of summing would decide between blocks next to
+// the border, in 64 only between those whose scores agree in all but their last bits (sums of queries and products with
+// bounds of 16 bits can span more than 53; the order is one for single tokens and another for trees); equal bounds give
+// equal scores within a call. The vector unit does them at the rate of 32 bits. Where lo or hi is infinite and its factor 0 the right side is no number, though the left one may be:
 // scores that are NaN are taken again without the products with 0.
 // k_select, k_select_few: the blocks of the largest scores, ties to the lowest index, by a search on the scores' bits.
 #include "cache_internal.h"
@@ -146,7 +147,7 @@ struct Range<UBW_E4M3> {
 
 // As many lanes as a row has 16 bytes go through a page of one head together, each with its own dims, several rows
 // requested at once: no lane needs another's. Bound: HBM (pages that 64 sequences filled in 80 layers, 97 MB: 18.2 us, 5.3
-// TB/s; a prompt of 50K positions, 435 MB: 78 us, 5.6 TB/s; before rows were requested ahead of the ones in use 91).
+// TB/s; a prompt of 50K positions, 435 MB: 78 us, 5.6 TB/s; before rows were requested ahead of the ones in use 91; the same in 8 bits, 218 MB: 44).
 template <int DT, int D>
 __global__ __launch_bounds__(256) void k_bounds(BoundsArgs a) {
     using E = Elems<DT>;
@@ -284,8 +285,8 @@ __device__ inline double group_sum(double x) {
     return x;
 }
 
-// One token a sequence: a workgroup takes kScoreBlocks blocks of a sequence and head. Bound: HBM or the Infinity Cache (64
-// ragged contexts, 251 MB of bounds: 40 us out of the latter, 52 out of memory; workgroups that stay and request ahead,
+// One token a sequence: a workgroup takes kScoreBlocks blocks of a sequence and head. Bound: HBM or the Infinity Cache,
+// with the vector unit busy 61% of the cycles (64 ragged contexts, 251 MB of bounds: 40 us out of the latter, 52 out of memory; workgroups that stay and request ahead,
 // or all heads of a block on one XCD, 54 and 58).
 template <int DT, typename TQ, int D>
 __global__ __launch_bounds__(256) void k_scores(SelectArgs a) {
@@ -349,7 +350,7 @@ __global__ __launch_bounds__(256) void k_scores(SelectArgs a) {
 // 16 tokens, its waves two times 16 blocks in turn.
 // Lane (c, j) holds of block c the 16-byte pieces j, j + 4, ..; the tokens' sums lie in LDS in the order of the
 // products' lanes. Bound: the 64-bit products (8 trees of 16 tokens over 40K to 130K positions, 8 heads, 1.4 GFLOP of
-// 78 TFLOP/s: 18 us of 40; 3 workgroups on most CUs, 6 us to sum up the queries).
+// 78 TFLOP/s: 18 us of 40, the matrix cores busy 56% of them; 3 workgroups on most CUs, 6 us to sum up the queries).
 template <int DT, typename TQ, int D>
 __global__ __launch_bounds__(256, D == 256 ? 2 : 1) void k_scores_tree(SelectArgs a) {
     using E = Elems<DT>;
